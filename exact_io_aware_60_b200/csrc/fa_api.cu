@@ -20,6 +20,8 @@
 #include "fa.h"
 #include "fa_fwd.cuh"
 #include "fa_bwd.cuh"
+#include "fa_paged.cuh"
+#include "fa_rope.cuh"
 
 namespace {
 
@@ -633,6 +635,220 @@ int launch_splitkv(const void *q, const void *k, const void *v, void *o, float *
     return FA_OK;
 }
 
+
+// ---------------------------------------------------------------- positions, paged cache
+
+// A [n0, n1, n2, d] 16-bit tensor: element strides from the caller (NULL: contiguous).
+// Rows are read and written in 16-byte vectors, so every stride of a dimension longer than
+// one has to be a multiple of 8 elements.
+// (an input may be broadcast, stride 0; an output or a cache may not)
+bool make_rows(fa::Rows *r, const void *p, const long long *strides, long long n0, long long n1,
+               long long n2, int d, bool broadcast) {
+    r->p = static_cast<const uint16_t *>(p);
+    if (strides == nullptr) {
+        r->st = d;
+        r->sh = n2 * d;
+        r->sb = n1 * n2 * d;
+        return true;
+    }
+    const long long n[3] = {n0, n1, n2};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (strides[i] % 8 != 0 || strides[i] < (broadcast ? 0 : 8))) return false;
+    r->sb = strides[0];
+    r->sh = strides[1];
+    r->st = strides[2];
+    return true;
+}
+
+// Sizes and rotation arguments shared by fa_rope and fa_kv_append.
+int check_rope(int d, const unsigned long long *turns, int rot_dim, int interleaved,
+               float magnitude) {
+    if (!turns || (reinterpret_cast<uintptr_t>(turns) & 7u)) return FA_ERR_INVALID_ARG;
+    if (rot_dim < 1 || rot_dim > d || (interleaved != 0 && interleaved != 1)) return FA_ERR_INVALID_ARG;
+    if (!std::isfinite(magnitude) || !(magnitude > 0.f)) return FA_ERR_INVALID_ARG;
+    return rot_dim % 16 != 0 ? FA_ERR_UNSUPPORTED : FA_OK;
+}
+
+// Block and grid of the kernels whose threads are (token, chunk) x heads: as many heads to a
+// thread as still leave about `kWant` threads, so that long calls reuse a token's sines for
+// 8 heads and short ones spread over the GPU.
+struct TokenGrid {
+    dim3 grid, block;
+    int heads_per_thread;
+};
+TokenGrid token_grid(long long tokens, int heads, int d) {
+    constexpr long long kWant = 148 * 1024;
+    const int cpt = d / 16;
+    TokenGrid g;
+    g.heads_per_thread = 1;
+    while (g.heads_per_thread < 8 && tokens * cpt * ((heads + 2 * g.heads_per_thread - 1) / (2 * g.heads_per_thread)) >= kWant)
+        g.heads_per_thread *= 2;
+    int tx = 1;
+    while (tx < 256 / cpt && tx < tokens) tx *= 2;
+    const int groups = (heads + g.heads_per_thread - 1) / g.heads_per_thread;
+    g.block = dim3((unsigned)(tx * cpt), (unsigned)(256 / (tx * cpt)));
+    g.grid = dim3((unsigned)((tokens + tx - 1) / tx), (unsigned)((groups + g.block.y - 1) / g.block.y));
+    return g;
+}
+
+// Calls f(bool bf16, bool interleaved, int d) with its arguments as compile-time constants.
+template <typename F>
+auto with_rope_types(bool bf16, bool inter, int d, F &&f) {
+    using T = std::true_type;
+    using N = std::false_type;
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    if (d == 64) {
+        if (bf16) return inter ? f(T{}, T{}, D64{}) : f(T{}, N{}, D64{});
+        return inter ? f(N{}, T{}, D64{}) : f(N{}, N{}, D64{});
+    }
+    if (bf16) return inter ? f(T{}, T{}, D128{}) : f(T{}, N{}, D128{});
+    return inter ? f(N{}, T{}, D128{}) : f(N{}, N{}, D128{});
+}
+
+int check_sizes(long long B, long long heads, long long N, int d, int dtype) {
+    if (B < 1 || heads < 1 || N < 1 || d < 1) return FA_ERR_INVALID_ARG;
+    if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if (B * N >= (1LL << 31) - 256 || B * heads >= (1LL << 31) || heads > 65535)
+        return FA_ERR_UNSUPPORTED;
+    if ((double)B * heads * N * d > (double)FA_MAX_ELEMENTS) return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+int rope_common(const void *q, void *q_out, const void *k, void *k_out, int B, int H, int Hk,
+                int N, int d, const long long *q_strides, const long long *q_out_strides,
+                const long long *k_strides, const long long *k_out_strides, const int *positions,
+                int positions_per_batch, const unsigned long long *turns, int rot_dim,
+                int interleaved, float magnitude, int dtype, void *stream, float sign) {
+    if (!q || !q_out || !aligned16(q) || !aligned16(q_out)) return FA_ERR_INVALID_ARG;
+    if ((k == nullptr) != (k_out == nullptr) || !aligned16(k) || !aligned16(k_out))
+        return FA_ERR_INVALID_ARG;
+    if (H < 1 || (k && Hk < 1)) return FA_ERR_INVALID_ARG;
+    if (positions && (reinterpret_cast<uintptr_t>(positions) & 3u)) return FA_ERR_INVALID_ARG;
+    if (positions_per_batch != 0 && positions_per_batch != 1) return FA_ERR_INVALID_ARG;
+    const long long heads = (long long)H + (k ? Hk : 0);
+    int rc = check_sizes(B, heads, N, d, dtype);
+    if (rc == FA_OK) rc = check_rope(d, turns, rot_dim, interleaved, magnitude);
+    if (rc != FA_OK) return rc;
+    fa::RopeParams p;
+    std::memset(&p, 0, sizeof(p));
+    if (!make_rows(&p.q, q, q_strides, B, H, N, d, true) || !make_rows(&p.qo, q_out, q_out_strides, B, H, N, d, false))
+        return FA_ERR_INVALID_ARG;
+    if (k && (!make_rows(&p.k, k, k_strides, B, Hk, N, d, true) ||
+              !make_rows(&p.ko, k_out, k_out_strides, B, Hk, N, d, false)))
+        return FA_ERR_INVALID_ARG;
+    int dev = 0;
+    rc = check_device(&dev);
+    if (rc != FA_OK) return rc;
+    p.H = H;
+    p.HT = (int)heads;
+    p.N = N;
+    p.tokens = B * N;
+    p.positions = positions;
+    p.positions_sb = positions_per_batch ? N : 0;
+    p.turns = turns;
+    p.rot = rot_dim;
+    p.mag = magnitude;
+    p.sign = sign;
+    const TokenGrid g = token_grid(p.tokens, p.HT, d);
+    p.heads_per_thread = g.heads_per_thread;
+    cudaError_t e = with_rope_types(dtype == FA_BF16, interleaved != 0, d, [&](auto bf, auto in, auto dd) {
+        return launch_pdl(fa::fa_rope_kernel<bf(), in(), dd()>, g.grid, g.block, 0,
+                          reinterpret_cast<cudaStream_t>(stream), p);
+    });
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) {
+        record_cuda_error(e, "fa_rope launch");
+        return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
+// Page table arguments (host side); page sizes are powers of two from 8.
+int make_pages(fa::PageTable *t, int num_pages, int page_size, const int *table, int max_blocks,
+               const int *cache_len, const int *new_len) {
+    if (!table || !cache_len || num_pages < 1 || max_blocks < 1 || page_size < 1)
+        return FA_ERR_INVALID_ARG;
+    for (const int *x : {table, cache_len, new_len})
+        if (reinterpret_cast<uintptr_t>(x) & 3u) return FA_ERR_INVALID_ARG;
+    if (page_size < 8 || (page_size & (page_size - 1)) != 0) return FA_ERR_UNSUPPORTED;
+    if ((long long)max_blocks * page_size >= (1LL << 31) - 256) return FA_ERR_UNSUPPORTED;
+    t->table = table;
+    t->max_blocks = max_blocks;
+    t->num_pages = num_pages;
+    t->page_shift = 0;
+    while ((1 << t->page_shift) < page_size) ++t->page_shift;
+    t->cache_len = cache_len;
+    t->new_len = new_len;
+    return FA_OK;
+}
+
+// 4-D view [pages][heads][rows of a page][d] of a cache with the given strides;
+// box = 64 elements x box_rows.
+bool make_cache_map(CUtensorMap *m, const fa::Rows &r, int bf16, int d, int page_size, int heads,
+                    int num_pages, int box_rows) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page_size, (cuuint64_t)heads, (cuuint64_t)num_pages};
+    // (a dimension of one entry may carry any stride: give it one that the encoder takes)
+    const long long s[3] = {r.st, heads > 1 ? r.sh : (long long)page_size * d,
+                            num_pages > 1 ? r.sb : (long long)page_size * d * heads};
+    cuuint64_t strides[3] = {(cuuint64_t)(s[0] * 2), (cuuint64_t)(s[1] * 2), (cuuint64_t)(s[2] * 2)};
+    cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult e = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                     const_cast<uint16_t *>(r.p), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (e != CUDA_SUCCESS) {
+        snprintf(t_last_error, sizeof(t_last_error), "cuTensorMapEncodeTiled failed (%d)", (int)e);
+        return false;
+    }
+    return true;
+}
+
+// Rows of a tile: the copies of the rows (REP) that fit 128 lanes.
+int paged_rows(long long R) { return R <= 32 ? 32 : (R <= 64 ? 64 : 128); }
+
+struct PagedWorkspace {
+    size_t o_bytes, total;
+};
+PagedWorkspace paged_workspace(long long R, int d, int ctas) {
+    const size_t rows = (size_t)2 * ctas * paged_rows(R);
+    PagedWorkspace w;
+    w.o_bytes = round256(rows * d * 4);
+    w.total = w.o_bytes + round256(rows * 4);
+    return w;
+}
+
+template <int D, bool BF16, int REP>
+int launch_paged(const CUtensorMap &mk, const CUtensorMap &mv, const fa::PagedParams &p, int cap_tiles,
+                 cudaStream_t st, int dev) {
+    using C = fa::PagedCfg<D>;
+    auto kern = fa::fa_paged_kernel<D, BF16, REP>;
+    static std::atomic<int> smem_done[kMaxDevices];
+    cudaError_t e = set_smem(kern, C::SMEM, smem_done, dev);
+    if (e != cudaSuccess) {
+        record_cuda_error(e, "cudaFuncSetAttribute(paged)");
+        return FA_ERR_CUDA;
+    }
+    constexpr int ROWS = 128 / REP;
+    e = launch_pdl(kern, dim3((unsigned)p.ctas), dim3(C::THREADS), C::SMEM, st, mk, mv, p);
+    if (e == cudaSuccess && cap_tiles > 1) {
+        const int rows = std::min((long long)ROWS, (long long)p.T * p.G);
+        e = launch_pdl(fa::fa_paged_merge_kernel<D, BF16>,
+                       dim3((unsigned)(p.B * p.Hk * p.row_tiles), (unsigned)((rows + 3) / 4)),
+                       dim3(128), 0, st, p, (int)ROWS);
+    }
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) {
+        record_cuda_error(e, "fa_fwd_paged launch");
+        return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -670,6 +886,7 @@ const char *fa_strerror(int status) {
         case FA_ERR_UNSUPPORTED: return "unsupported configuration or device";
         case FA_ERR_CUDA: return "CUDA error";
         case FA_ERR_TIMEOUT: return "device-side wait timed out";
+        case FA_ERR_BAD_PAGE: return "page number or length outside the paged cache";
         case FA_ERR_SCRATCH_LIMIT: return "problem needs more scratch than fa_bwd_noalloc's static buffer";
         default: return "unknown status";
     }
@@ -948,7 +1165,157 @@ int fa_get_device_status(void *stream) {
         record_cuda_error(e, "status word");
         return FA_ERR_CUDA;
     }
+    if (val == 6) return FA_ERR_BAD_PAGE;
     return val == 0 ? FA_OK : FA_ERR_TIMEOUT;
+}
+
+int fa_rope(const void *q, void *q_out, const void *k, void *k_out, int B, int H, int Hk, int N,
+            int d, const long long *q_strides, const long long *q_out_strides,
+            const long long *k_strides, const long long *k_out_strides, const int *positions,
+            int positions_per_batch, const unsigned long long *turns, int rot_dim, int interleaved,
+            float magnitude, int dtype, void *stream) {
+    return rope_common(q, q_out, k, k_out, B, H, Hk, N, d, q_strides, q_out_strides, k_strides,
+                       k_out_strides, positions, positions_per_batch, turns, rot_dim, interleaved,
+                       magnitude, dtype, stream, 1.f);
+}
+
+int fa_rope_bwd(const void *dq_rot, void *dq, const void *dk_rot, void *dk, int B, int H, int Hk,
+                int N, int d, const long long *dq_rot_strides, const long long *dq_strides,
+                const long long *dk_rot_strides, const long long *dk_strides, const int *positions,
+                int positions_per_batch, const unsigned long long *turns, int rot_dim,
+                int interleaved, float magnitude, int dtype, void *stream) {
+    return rope_common(dq_rot, dq, dk_rot, dk, B, H, Hk, N, d, dq_rot_strides, dq_strides,
+                       dk_rot_strides, dk_strides, positions, positions_per_batch, turns, rot_dim,
+                       interleaved, magnitude, dtype, stream, -1.f);
+}
+
+int fa_kv_append(const void *k, const void *v, void *k_cache, void *v_cache, const void *q,
+                 void *q_out, int B, int H, int Hk, int T, int d, const long long *k_strides,
+                 const long long *v_strides, const long long *q_strides,
+                 const long long *q_out_strides, const long long *k_cache_strides,
+                 const long long *v_cache_strides, int num_pages, int page_size,
+                 const int *block_table, int max_blocks, const int *cache_len, const int *new_len,
+                 const int *positions, const unsigned long long *turns, int rot_dim,
+                 int interleaved, float magnitude, int dtype, void *stream) {
+    if (!k || !v || !k_cache || !v_cache || (q == nullptr) != (q_out == nullptr))
+        return FA_ERR_INVALID_ARG;
+    for (const void *x : {k, v, (const void *)k_cache, (const void *)v_cache, q, (const void *)q_out})
+        if (!aligned16(x)) return FA_ERR_INVALID_ARG;
+    if (Hk < 1 || (q && H < 1)) return FA_ERR_INVALID_ARG;
+    if (positions && (reinterpret_cast<uintptr_t>(positions) & 3u)) return FA_ERR_INVALID_ARG;
+    const long long heads = (q ? (long long)H : 0) + 2LL * Hk;
+    int rc = check_sizes(B, heads, T, d, dtype);
+    fa::AppendParams p;
+    std::memset(&p, 0, sizeof(p));
+    if (rc == FA_OK) rc = make_pages(&p.pt, num_pages, page_size, block_table, max_blocks, cache_len, new_len);
+    if (rc == FA_OK && turns) rc = check_rope(d, turns, rot_dim, interleaved, magnitude);
+    if (rc != FA_OK) return rc;
+    if ((double)num_pages * Hk * page_size * d > (double)FA_MAX_ELEMENTS) return FA_ERR_UNSUPPORTED;
+    if (!make_rows(&p.k, k, k_strides, B, Hk, T, d, true) || !make_rows(&p.v, v, v_strides, B, Hk, T, d, true) ||
+        !make_rows(&p.kc, k_cache, k_cache_strides, num_pages, Hk, page_size, d, false) ||
+        !make_rows(&p.vc, v_cache, v_cache_strides, num_pages, Hk, page_size, d, false))
+        return FA_ERR_INVALID_ARG;
+    if (q && (!make_rows(&p.q, q, q_strides, B, H, T, d, true) ||
+              !make_rows(&p.qo, q_out, q_out_strides, B, H, T, d, false)))
+        return FA_ERR_INVALID_ARG;
+    int dev = 0;
+    rc = check_device(&dev);
+    if (rc != FA_OK) return rc;
+    p.H = q ? H : 0;
+    p.Hk = Hk;
+    p.HT = (int)heads;
+    p.T = T;
+    p.tokens = B * T;
+    p.positions = positions;
+    p.turns = turns;
+    p.rot = rot_dim;
+    p.mag = magnitude;
+    const TokenGrid g = token_grid(p.tokens, p.HT, d);
+    p.heads_per_thread = g.heads_per_thread;
+    cudaError_t e = with_rope_types(dtype == FA_BF16, turns && interleaved, d, [&](auto bf, auto in, auto dd) {
+        return launch_pdl(fa::fa_kv_append_kernel<bf(), in(), dd()>, g.grid, g.block, 0,
+                          reinterpret_cast<cudaStream_t>(stream), p);
+    });
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) {
+        record_cuda_error(e, "fa_kv_append launch");
+        return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
+size_t fa_fwd_paged_workspace_bytes(int B, int H, int Hk, int T, int d) {
+    if (B < 1 || Hk < 1 || H < Hk || H % Hk != 0 || T < 1 || (d != 64 && d != 128)) return 0;
+    return paged_workspace((long long)T * (H / Hk), d, current_sms()).total;
+}
+
+int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *o, float *lse, int B,
+                 int H, int Hk, int T, int d, const long long *q_strides,
+                 const long long *o_strides, const long long *k_cache_strides,
+                 const long long *v_cache_strides, int num_pages, int page_size,
+                 const int *block_table, int max_blocks, const int *cache_len, const int *new_len,
+                 const unsigned char *tree_mask, int tree_per_batch, float scale, int dtype,
+                 void *workspace, size_t workspace_bytes, void *stream) {
+    if (!q || !k_cache || !v_cache || !o || !lse) return FA_ERR_INVALID_ARG;
+    for (const void *x : {q, k_cache, v_cache, (const void *)o})
+        if (!aligned16(x)) return FA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(lse) & 3u) return FA_ERR_INVALID_ARG;
+    if (H < 1 || Hk < 1 || H % Hk != 0) return FA_ERR_INVALID_ARG;
+    if (tree_per_batch != 0 && tree_per_batch != 1) return FA_ERR_INVALID_ARG;
+    int rc = check_sizes(B, H, T, d, dtype);
+    if (rc != FA_OK) return rc;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+    fa::PagedParams p;
+    std::memset(&p, 0, sizeof(p));
+    rc = make_pages(&p.pt, num_pages, page_size, block_table, max_blocks, cache_len, new_len);
+    if (rc != FA_OK) return rc;
+    if ((double)num_pages * Hk * page_size * d > (double)FA_MAX_ELEMENTS) return FA_ERR_UNSUPPORTED;
+    fa::Rows kc;
+    if (!make_rows(&p.q, q, q_strides, B, H, T, d, true) || !make_rows(&p.o, o, o_strides, B, H, T, d, false) ||
+        !make_rows(&kc, k_cache, k_cache_strides, num_pages, Hk, page_size, d, false) ||
+        !make_rows(&p.vc, v_cache, v_cache_strides, num_pages, Hk, page_size, d, false))
+        return FA_ERR_INVALID_ARG;
+    const int G = H / Hk;
+    const long long R = (long long)T * G;
+    const int rows = paged_rows(R);
+    const long long row_tiles = (R + rows - 1) / rows;
+    const long long cap_tiles = ((long long)max_blocks * page_size + 127) / 128;
+    // units of one sequence and items of the call are counted in 32 bits
+    if (R >= (1LL << 31) - 256 || row_tiles * Hk * std::max(cap_tiles, 1LL) >= (1LL << 31) ||
+        row_tiles * Hk * B >= (1LL << 31))
+        return FA_ERR_UNSUPPORTED;
+    int dev = 0;
+    rc = check_device(&dev);
+    if (rc != FA_OK) return rc;
+    const int ctas = current_sms();
+    const PagedWorkspace ws = paged_workspace(R, d, ctas);
+    if (!workspace || workspace_bytes < ws.total || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return FA_ERR_INVALID_ARG;
+    p.lse = lse;
+    p.tree = tree_mask;
+    p.tree_sb = tree_per_batch ? (long long)T * T : 0;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + ws.o_bytes);
+    p.B = B;
+    p.Hk = Hk;
+    p.G = G;
+    p.T = T;
+    p.row_tiles = (int)row_tiles;
+    p.ctas = (int)std::min<long long>(ctas, row_tiles * Hk * B * std::max(cap_tiles, 1LL));
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const bool bf16 = dtype == FA_BF16;
+    CUtensorMap mk, mv;
+    const int box_rows = std::min(page_size, 128);
+    if (!make_cache_map(&mk, kc, bf16, d, page_size, Hk, num_pages, box_rows) ||
+        !make_cache_map(&mv, p.vc, bf16, d, page_size, Hk, num_pages, box_rows))
+        return FA_ERR_CUDA;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+#define FA_PAGED(D, BF) (rows == 32 ? launch_paged<D, BF, 4>(mk, mv, p, (int)cap_tiles, st, dev) \
+                         : rows == 64 ? launch_paged<D, BF, 2>(mk, mv, p, (int)cap_tiles, st, dev) \
+                                      : launch_paged<D, BF, 1>(mk, mv, p, (int)cap_tiles, st, dev))
+    if (d == 64) return bf16 ? FA_PAGED(64, true) : FA_PAGED(64, false);
+    return bf16 ? FA_PAGED(128, true) : FA_PAGED(128, false);
+#undef FA_PAGED
 }
 
 }  // extern "C"

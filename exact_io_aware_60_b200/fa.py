@@ -10,7 +10,10 @@ error, a :class:`FAError` is raised: there is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import dataclasses
+import math
 import os
 import threading
 from typing import Optional
@@ -22,6 +25,7 @@ LIB_PATH = os.path.join(_HERE, "libfa.so")
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = range(5)
 FA_ERR_SCRATCH_LIMIT = 5
+FA_ERR_BAD_PAGE = 6
 FA_NOALLOC_SCRATCH_BYTES = 64 << 20
 FA_BF16, FA_FP16 = 0, 1
 
@@ -96,6 +100,18 @@ def lib():
             L.fa_bwd_noalloc.restype = i
             L.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i,
                                          vp, i, vp]
+            L.fa_rope.restype = i
+            L.fa_rope.argtypes = [vp] * 4 + [i] * 5 + [vp] * 5 + [i, vp, i, i, f, i, vp]
+            L.fa_rope_bwd.restype = i
+            L.fa_rope_bwd.argtypes = L.fa_rope.argtypes
+            L.fa_kv_append.restype = i
+            L.fa_kv_append.argtypes = ([vp] * 6 + [i] * 5 + [vp] * 6 + [i, i, vp, i] + [vp] * 4
+                                       + [i, i, f, i, vp])
+            L.fa_fwd_paged_workspace_bytes.restype = sz
+            L.fa_fwd_paged_workspace_bytes.argtypes = [i] * 5
+            L.fa_fwd_paged.restype = i
+            L.fa_fwd_paged.argtypes = ([vp] * 5 + [i] * 5 + [vp] * 4 + [i, i, vp, i] + [vp] * 3
+                                       + [i, f, i, vp, sz, vp])
             L.fa_schedule_items.restype = i
             L.fa_schedule_items.argtypes = [vp, i, i, vp, vp]
             _lib = L
@@ -106,7 +122,8 @@ def fa_strerror(status: int) -> str:
     if _lib is None:
         return {0: "ok", 1: "invalid argument", 2: "unsupported configuration or device",
                 3: "CUDA error", 4: "device-side wait timed out",
-                5: "problem needs more scratch than fa_bwd_noalloc's static buffer"}.get(
+                5: "problem needs more scratch than fa_bwd_noalloc's static buffer",
+                6: "page number or length outside the paged cache"}.get(
                     status, "unknown status")
     return _lib.fa_strerror(int(status)).decode()
 
@@ -383,6 +400,288 @@ def fa_fwd_fp8(q8, k8, v8, o, lse, *, scale: float, q_scale: float, k_scale: flo
         raise FAError(rc, "fa_fwd_fp8")
 
 
+# ------------------------------------------------------------------ rotary positions
+
+@dataclasses.dataclass(frozen=True)
+class RopePlan:
+    """What :func:`fa_rope` and :func:`fa_kv_append` rotate by (made by :func:`rope_plan`).
+
+    ``turns``: int64 CUDA tensor [rot_dim / 2], each pair's angle per position as a fraction
+    of a turn in units of 2^-64 (the bits of the unsigned value of include/fa.h)."""
+    turns: torch.Tensor
+    rot_dim: int
+    interleaved: bool
+    magnitude: float
+
+
+def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, original_length: Optional[int] = None,
+                     beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(f, magnitude): the angle per position of each pair, a list of rot_dim / 2 floats in
+    64 bits, and the factor of the rotated elements.
+
+    f_i = base^(-2 i / rot_dim), scaled for contexts ``factor`` times as long by
+
+    * ``"linear"`` (position interpolation): f_i / factor;
+    * ``"ntk"``: base multiplied by factor^(rot_dim / (rot_dim - 2)), so that the slowest
+      pair is scaled by 1 / factor and the fastest not at all;
+    * ``"yarn"`` (YaRN, Peng et al. 2023): pairs that turn more than ``beta_fast`` times
+      within ``original_length`` keep f_i, those below ``beta_slow`` get f_i / factor, a
+      linear ramp in between; the magnitude is 0.1 ln(factor) + 1."""
+    if rot_dim < 2 or rot_dim % 2 or not (math.isfinite(base) and base > 0.0):
+        raise FAError(FA_ERR_INVALID_ARG, "rope_frequencies: rot_dim even and >= 2, base > 0")
+    if not (math.isfinite(factor) and factor >= 1.0):
+        raise FAError(FA_ERR_INVALID_ARG, "rope_frequencies: factor must be finite and >= 1")
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise FAError(FA_ERR_INVALID_ARG, f"rope_frequencies: unknown scaling {scaling!r}")
+    if scaling == "ntk":
+        if rot_dim == 2:
+            raise FAError(FA_ERR_INVALID_ARG, "rope_frequencies: ntk needs rot_dim > 2")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = [base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+    if scaling == "linear":
+        return [x / factor for x in f], 1.0
+    if scaling == "yarn":
+        if original_length is None or original_length < 1 or not beta_fast > beta_slow:
+            raise FAError(FA_ERR_INVALID_ARG, "rope_frequencies: yarn needs original_length >= 1 "
+                                              "and beta_fast > beta_slow")
+        out = []
+        for x in f:
+            r = original_length * x / (2.0 * math.pi)
+            keep = min(max((r - beta_slow) / (beta_fast - beta_slow), 0.0), 1.0)
+            out.append((1.0 - keep) * x / factor + keep * x)
+        return out, 0.1 * math.log(factor) + 1.0
+    return f, 1.0
+
+
+def rope_plan(rot_dim: int, *, layout: str = "half", base: float = 10000.0, scaling: str = "none",
+              factor: float = 1.0, original_length: Optional[int] = None,
+              beta_fast: float = 32.0, beta_slow: float = 1.0, frequencies=None,
+              magnitude: Optional[float] = None, device=None) -> RopePlan:
+    """A rotation plan, made once and kept.  ``layout``: "half" (pairs (i, i + rot_dim / 2))
+    or "interleaved" (pairs (2 i, 2 i + 1)).  The frequencies are :func:`rope_frequencies`'s,
+    or ``frequencies``: rot_dim / 2 angles per position in radians; ``magnitude`` overrides
+    the scaling's factor of the rotated elements."""
+    if layout not in ("half", "interleaved"):
+        raise FAError(FA_ERR_INVALID_ARG, f"rope_plan: unknown layout {layout!r}")
+    if rot_dim < 16 or rot_dim % 16:
+        raise FAError(FA_ERR_UNSUPPORTED, "rope_plan: rot_dim must be a positive multiple of 16")
+    if frequencies is None:
+        freq, mag = rope_frequencies(rot_dim, base=base, scaling=scaling, factor=factor,
+                                     original_length=original_length, beta_fast=beta_fast,
+                                     beta_slow=beta_slow)
+    else:
+        freq, mag = [float(x) for x in frequencies], 1.0
+        if len(freq) != rot_dim // 2 or not all(math.isfinite(x) for x in freq):
+            raise FAError(FA_ERR_INVALID_ARG, "rope_plan: frequencies must be rot_dim / 2 finite "
+                                              "numbers")
+    mag = mag if magnitude is None else float(magnitude)
+    if not (math.isfinite(mag) and mag > 0.0):
+        raise FAError(FA_ERR_INVALID_ARG, "rope_plan: magnitude must be finite and > 0")
+    turns = []
+    for x in freq:
+        u = int(round(x / (2.0 * math.pi) * 2.0 ** 64)) % (1 << 64)
+        turns.append(u - (1 << 64) if u >= 1 << 63 else u)
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return RopePlan(torch.tensor(turns, dtype=torch.int64, device=device), rot_dim,
+                    layout == "interleaved", mag)
+
+
+_I3 = ctypes.c_longlong * 3
+
+
+def _rows(t, name: str, shape, dtype, device):
+    """Checks a [.., .., .., d] tensor with d contiguous; its strides for the library (None if
+    contiguous)."""
+    if not isinstance(t, torch.Tensor):
+        raise FAError(FA_ERR_INVALID_ARG, f"{name} must be a torch.Tensor")
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        raise FAError(FA_ERR_INVALID_ARG,
+                      f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} "
+                      f"{tuple(t.shape)} on {t.device}")
+    if t.is_contiguous():
+        return None
+    st = t.stride()
+    if st[3] != 1:
+        raise FAError(FA_ERR_INVALID_ARG, f"{name}: the last dimension must be contiguous")
+    return _I3(st[0], st[1], st[2])
+
+
+def _ints(t, name: str, shapes, device, dtype=torch.int32):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device \
+            or tuple(t.shape) not in shapes or not t.is_contiguous():
+        raise FAError(FA_ERR_INVALID_ARG,
+                      f"{name} must be a contiguous {dtype} tensor on {device}, shape "
+                      + " or ".join(str(s) for s in shapes))
+    return t.data_ptr()
+
+
+def _main(t, name: str) -> torch.device:
+    """The device of a call: that of its first tensor, [.., .., .., d] bf16 or fp16."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
+        raise FAError(FA_ERR_INVALID_ARG, f"{name} must be a 4-dimensional CUDA tensor")
+    return t.device
+
+
+class _On:
+    """The call's device and stream: the tensors' device is made current for the call, and the
+    stream is that device's current one unless the caller gives another."""
+    __slots__ = ("index", "before", "stream")
+
+    def __init__(self, device, stream):
+        self.index, self.stream = device.index, stream
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+        return _stream_handle(self.stream)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+        return False
+
+
+def _plan_args(plan, device):
+    if not isinstance(plan, RopePlan):
+        raise FAError(FA_ERR_INVALID_ARG, "the rotation must be a RopePlan (see rope_plan)")
+    _ints(plan.turns, "plan.turns", ((plan.rot_dim // 2,),), device, torch.int64)
+    return plan.turns.data_ptr(), plan.rot_dim, int(plan.interleaved), plan.magnitude
+
+
+def _rope_call(fn, where, x, x_out, plan, y, y_out, positions, stream, names):
+    device = _main(x, names[0])
+    B, H, N, d = x.shape
+    xs = _rows(x, names[0], x.shape, x.dtype, device)
+    xos = _rows(x_out, names[1], x.shape, x.dtype, device)
+    if (y is None) != (y_out is None):
+        raise FAError(FA_ERR_INVALID_ARG, f"{names[2]} and {names[3]} go together")
+    yp = yop = ys = yos = None
+    Hk = 0
+    if y is not None:
+        Hk = y.shape[1] if isinstance(y, torch.Tensor) and y.dim() == 4 else 0
+        shape = torch.Size((B, Hk, N, d))
+        ys = _rows(y, names[2], shape, x.dtype, device)
+        yos = _rows(y_out, names[3], shape, x.dtype, device)
+        yp, yop = y.data_ptr(), y_out.data_ptr()
+    pp, per_batch = None, 0
+    if positions is not None:
+        pp = _ints(positions, "positions", ((N,), (B, N)), device)
+        per_batch = int(positions.dim() == 2)
+    turns, rot, inter, mag = _plan_args(plan, device)
+    with _On(device, stream) as st:
+        rc = fn(x.data_ptr(), x_out.data_ptr(), yp, yop, B, H, Hk, N, d, xs, xos, ys, yos, pp,
+                per_batch, turns, rot, inter, mag, _dtype_code(x), st)
+    if rc != FA_OK:
+        raise FAError(rc, where)
+
+
+def fa_rope(q, q_out, plan: RopePlan, *, k=None, k_out=None, positions=None, stream=None) -> None:
+    """Rotary positions: writes ``q_out`` [B,H,N,d] (and ``k_out`` [B,Hk,N,d]) from ``q`` (and
+    ``k``) in one launch; ``q_out`` may be ``q``.  Strided views with a contiguous last
+    dimension are taken as they are.  ``positions``: int32 [N] or [B,N], None for 0 .. N-1."""
+    _rope_call(lib().fa_rope, "fa_rope", q, q_out, plan, k, k_out, positions, stream,
+               ("q", "q_out", "k", "k_out"))
+
+
+def fa_rope_bwd(dq_rot, dq, plan: RopePlan, *, k=None, k_out=None, positions=None,
+                stream=None) -> None:
+    """Backward pass of :func:`fa_rope`: gradients of its inputs from those of its outputs.
+    ``dq_rot`` -> ``dq``, and ``k`` (the gradient of the rotated keys) -> ``k_out``."""
+    _rope_call(lib().fa_rope_bwd, "fa_rope_bwd", dq_rot, dq, plan, k, k_out, positions, stream,
+               ("dq_rot", "dq", "k", "k_out"))
+
+
+# ------------------------------------------------------------------ paged cache
+
+def _cache_args(k_cache, v_cache, block_table, cache_len, new_len, B, Hk, d, dtype, device):
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise FAError(FA_ERR_INVALID_ARG, "k_cache must be a [pages, Hk, page_size, d] tensor")
+    P, hk, page, dc = k_cache.shape
+    if hk != Hk or dc != d:
+        raise FAError(FA_ERR_INVALID_ARG, f"k_cache: expected [pages, {Hk}, page_size, {d}], got "
+                                          f"{tuple(k_cache.shape)}")
+    ks = _rows(k_cache, "k_cache", k_cache.shape, dtype, device)
+    vs = _rows(v_cache, "v_cache", k_cache.shape, dtype, device)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise FAError(FA_ERR_INVALID_ARG, "block_table must be an int32 [B, max_blocks] tensor")
+    blocks = block_table.shape[1]
+    table = _ints(block_table, "block_table", ((B, blocks),), device)
+    held = _ints(cache_len, "cache_len", ((B,),), device)
+    new = None if new_len is None else _ints(new_len, "new_len", ((B,),), device)
+    return ks, vs, P, page, table, blocks, held, new
+
+
+def fa_kv_append(k, v, k_cache, v_cache, block_table, cache_len, *, new_len=None,
+                 rope: Optional[RopePlan] = None, positions=None, q=None, q_out=None,
+                 stream=None) -> None:
+    """Appends new keys and values ``k``, ``v`` [B,Hk,T,d] to a paged cache [pages,Hk,page_size,d],
+    keys (and queries ``q`` -> ``q_out`` [B,H,T,d]) rotated by ``rope`` on the way.  Token t
+    of sequence b goes to slot ``cache_len[b] + t`` (see include/fa.h); the lengths are not
+    advanced.  ``new_len``: int32 [B], None for T each; ``positions``: int32 [B,T], None for
+    the slots' own.  Strided views with a contiguous last dimension are taken as they are."""
+    device = _main(k, "k")
+    B, Hk, T, d = k.shape
+    ks = _rows(k, "k", k.shape, k.dtype, device)
+    vs = _rows(v, "v", k.shape, k.dtype, device)
+    kcs, vcs, P, page, table, blocks, held, new = _cache_args(
+        k_cache, v_cache, block_table, cache_len, new_len, B, Hk, d, k.dtype, device)
+    if (q is None) != (q_out is None):
+        raise FAError(FA_ERR_INVALID_ARG, "q and q_out go together")
+    qp = qop = qs = qos = None
+    H = 0
+    if q is not None:
+        H = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 4 else 0
+        shape = torch.Size((B, H, T, d))
+        qs = _rows(q, "q", shape, k.dtype, device)
+        qos = _rows(q_out, "q_out", shape, k.dtype, device)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    pp = None if positions is None else _ints(positions, "positions", ((B, T),), device)
+    turns, rot, inter, mag = (None, 0, 0, 1.0) if rope is None else _plan_args(rope, device)
+    with _On(device, stream) as st:
+        rc = lib().fa_kv_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                qp, qop, B, H, Hk, T, d, ks, vs, qs, qos, kcs, vcs, P, page, table,
+                                blocks, held, new, pp, turns, rot, inter, mag, _dtype_code(k), st)
+    if rc != FA_OK:
+        raise FAError(rc, "fa_kv_append")
+
+
+def fa_fwd_paged_workspace_bytes(B: int, H: int, Hk: int, T: int, d: int) -> int:
+    return int(lib().fa_fwd_paged_workspace_bytes(B, H, Hk, T, d))
+
+
+def fa_fwd_paged(q, k_cache, v_cache, block_table, cache_len, o, lse, *, scale: float,
+                 new_len=None, tree_mask=None, workspace: torch.Tensor, stream=None) -> None:
+    """Attention of the new tokens ``q`` [B,H,T,d] over a paged cache that already holds their
+    keys and values: writes ``o`` [B,H,T,d] and ``lse`` [B,H,T].  ``tree_mask``: uint8 [T,T] or
+    [B,T,T] (row = token, column = new key it sees), None for a chain.  ``workspace``: uint8
+    CUDA tensor of ``fa_fwd_paged_workspace_bytes`` bytes.  See include/fa.h."""
+    device = _main(q, "q")
+    B, H, T, d = q.shape
+    qs = _rows(q, "q", q.shape, q.dtype, device)
+    os_ = _rows(o, "o", q.shape, q.dtype, device)
+    Hk = k_cache.shape[1] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else 0
+    kcs, vcs, P, page, table, blocks, held, new = _cache_args(
+        k_cache, v_cache, block_table, cache_len, new_len, B, Hk, d, q.dtype, device)
+    lp = _ints(lse, "lse", ((B, H, T),), device, torch.float32)
+    tp, per_batch = None, 0
+    if tree_mask is not None:
+        tp = _ints(tree_mask, "tree_mask", ((T, T), (B, T, T)), device, torch.uint8)
+        per_batch = int(tree_mask.dim() == 3)
+    if not isinstance(workspace, torch.Tensor) or workspace.device != device \
+            or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise FAError(FA_ERR_INVALID_ARG, f"workspace must be a contiguous uint8 tensor on {device}")
+    with _On(device, stream) as st:
+        rc = lib().fa_fwd_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
+                                lp, B, H, Hk, T, d, qs, os_, kcs, vcs, P, page, table, blocks,
+                                held, new, tp, per_batch, float(scale), _dtype_code(q),
+                                workspace.data_ptr(), workspace.numel(), st)
+    if rc != FA_OK:
+        raise FAError(rc, "fa_fwd_paged")
+
+
 def fa_set_timing_events(which: int, start=None, stop=None) -> None:
     """Profiling hook: record torch.cuda.Event ``start``/``stop`` around every launch of
     the forward kernel (which=0) or the backward main kernel (which=1); None switches it
@@ -436,3 +735,100 @@ def backward(q, k, v, o, dout, lse, *, scale: Optional[float] = None, causal: bo
     fa_bwd(q, k, v, o, dout, lse, dq, dk, dv, scale=scale, causal=causal, kv_len=kv_len,
            workspace=workspace, stream=stream)
     return dq, dk, dv
+
+
+@contextlib.contextmanager
+def _allocating(t, name: str, stream):
+    """The helpers below allocate on the tensors' device and in the call's stream, so that a
+    temporary's memory is reused only after the kernels that still read it."""
+    with _On(_main(t, name), stream):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def rope(q, plan: RopePlan, *, k=None, positions=None, stream=None):
+    """Allocates the outputs with torch and runs :func:`fa_rope`; returns ``q_rot``, or
+    ``(q_rot, k_rot)`` with keys."""
+    with _allocating(q, "q", stream):
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        k_out = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
+        fa_rope(q, q_out, plan, k=k, k_out=k_out, positions=positions, stream=stream)
+    return q_out if k is None else (q_out, k_out)
+
+
+def rope_backward(dq_rot, plan: RopePlan, *, dk_rot=None, positions=None, stream=None):
+    """Allocates the outputs with torch and runs :func:`fa_rope_bwd`; returns ``dq``, or
+    ``(dq, dk)``."""
+    with _allocating(dq_rot, "dq_rot", stream):
+        dq = torch.empty_like(dq_rot, memory_format=torch.contiguous_format)
+        dk = None if dk_rot is None else torch.empty_like(dk_rot,
+                                                          memory_format=torch.contiguous_format)
+        fa_rope_bwd(dq_rot, dq, plan, k=dk_rot, k_out=dk, positions=positions, stream=stream)
+    return dq if dk_rot is None else (dq, dk)
+
+
+def forward_rope(q, k, v, plan: RopePlan, *, positions=None, scale: Optional[float] = None,
+                 causal: bool = False, kv_len=None, stream=None):
+    """:func:`fa_rope` of q and k, then :func:`forward`: returns ``(o, lse, q_rot, k_rot)``,
+    the last two for :func:`backward_rope`."""
+    with _allocating(q, "q", stream):
+        q_rot, k_rot = rope(q, plan, k=k, positions=positions, stream=stream)
+        o, lse = forward(q_rot, k_rot, v, scale=scale, causal=causal, kv_len=kv_len, stream=stream)
+    return o, lse, q_rot, k_rot
+
+
+def backward_rope(q_rot, k_rot, v, o, dout, lse, plan: RopePlan, *, positions=None,
+                  scale: Optional[float] = None, causal: bool = False, kv_len=None,
+                  workspace=None, stream=None):
+    """Gradients of :func:`forward_rope`'s q, k, v: :func:`backward`, then dq and dk turned back
+    in place."""
+    with _allocating(q_rot, "q_rot", stream):
+        dq, dk, dv = backward(q_rot, k_rot, v, o, dout, lse, scale=scale, causal=causal,
+                              kv_len=kv_len, workspace=workspace, stream=stream)
+        fa_rope_bwd(dq, dq, plan, k=dk, k_out=dk, positions=positions, stream=stream)
+    return dq, dk, dv
+
+
+def paged_workspace_for(q, Hk: int, stream=None) -> torch.Tensor:
+    """A workspace for :func:`fa_fwd_paged` calls of q's shape with ``Hk`` key/value heads."""
+    B, H, T, d = q.shape
+    with _allocating(q, "q", stream):
+        return torch.empty(fa_fwd_paged_workspace_bytes(B, H, Hk, T, d), dtype=torch.uint8,
+                           device=q.device)
+
+
+def forward_paged(q, k_cache, v_cache, block_table, cache_len, *, scale: Optional[float] = None,
+                  new_len=None, tree_mask=None, workspace=None, stream=None):
+    """Allocates ``o``, ``lse`` (and the workspace if not given) with torch and runs
+    :func:`fa_fwd_paged`."""
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    with _allocating(q, "q", stream):
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = paged_workspace_for(q, k_cache.shape[1], stream)
+        fa_fwd_paged(q, k_cache, v_cache, block_table, cache_len, o, lse, scale=scale,
+                     new_len=new_len, tree_mask=tree_mask, workspace=workspace, stream=stream)
+    return o, lse
+
+
+def step_paged(q, k, v, k_cache, v_cache, block_table, cache_len, *,
+               rope: Optional[RopePlan] = None, positions=None, scale: Optional[float] = None,
+               new_len=None, tree_mask=None, workspace=None, stream=None):
+    """A serving step's attention: :func:`fa_kv_append` of the new tokens (q and k rotated by
+    ``rope``), then :func:`forward_paged` over the cache.  Returns ``(o, lse)``; the caller
+    advances ``cache_len`` once the tokens are accepted."""
+    with _allocating(q, "q", stream):
+        q_rot = None
+        if rope is not None:
+            q_rot = torch.empty_like(q, memory_format=torch.contiguous_format)
+        fa_kv_append(k, v, k_cache, v_cache, block_table, cache_len, new_len=new_len, rope=rope,
+                     positions=positions, q=None if rope is None else q, q_out=q_rot,
+                     stream=stream)
+        return forward_paged(q if rope is None else q_rot, k_cache, v_cache, block_table,
+                             cache_len, scale=scale, new_len=new_len, tree_mask=tree_mask,
+                             workspace=workspace, stream=stream)

@@ -67,7 +67,8 @@ typedef enum {
     FA_ERR_UNSUPPORTED = 2,
     FA_ERR_CUDA = 3,
     FA_ERR_TIMEOUT = 4,
-    FA_ERR_SCRATCH_LIMIT = 5
+    FA_ERR_SCRATCH_LIMIT = 5,
+    FA_ERR_BAD_PAGE = 6
 } fa_status;
 
 typedef enum { FA_BF16 = 0, FA_FP16 = 1 } fa_dtype;
@@ -124,7 +125,9 @@ FA_API const char *fa_last_cuda_error(void);
 /*
  * Synchronises `stream`, then reads and clears the current device's status word.
  * Returns FA_OK, FA_ERR_TIMEOUT if some kernel gave up a bounded wait since the
- * last call, or FA_ERR_CUDA if the synchronisation failed.
+ * last call, FA_ERR_BAD_PAGE if a paged-cache call met a page number or a length outside
+ * the cache (the later of the two where both happened), or FA_ERR_CUDA if the
+ * synchronisation failed.
  */
 FA_API int fa_get_device_status(void *stream);
 
@@ -301,6 +304,121 @@ FA_API int fa_bwd_noalloc(const void *q, const void *k, const void *v, const voi
                           const void *dout, const float *lse, void *dq, void *dk, void *dv,
                           int B, int H, int N, int d, float scale, int causal,
                           const int *kv_len, int dtype, void *stream);
+
+/*
+ * Rotary positions.  Pair i (0 <= i < rot_dim / 2) of the first rot_dim elements of every
+ * head, at position p, turns by the angle a = p f_i:
+ *     (y1, y2) = magnitude * (x1 cos a - x2 sin a, x2 cos a + x1 sin a)
+ * with (x1, x2) = (x[i], x[i + rot_dim / 2]) in the half layout (interleaved = 0) and
+ * (x[2 i], x[2 i + 1]) in the interleaved one (interleaved = 1).  Elements from rot_dim on
+ * are copied.  Computed in fp32 from the angle's exact fraction of a turn, rounded once.
+ *   q, q_out    : DEVICE [B, H, N, d] 16-bit, read / written.  q_out may be q (in place, same
+ *                 strides); otherwise the tensors must not overlap.
+ *   k, k_out    : DEVICE [B, Hk, N, d], or both NULL (Hk is then ignored).  Same launch.
+ *   *_strides   : HOST array of three element strides (batch, head, token), or NULL for a
+ *                 contiguous tensor; d is contiguous.  Strides of dimensions longer than one
+ *                 are multiples of 8, positive (0, a broadcast, is allowed for q and k).
+ *   positions   : DEVICE int32, [N] (positions_per_batch = 0) or [B, N] (1), or NULL for
+ *                 0 .. N-1.  Any int32 value.
+ *   turns       : DEVICE [rot_dim / 2], f_i as a fraction of a turn per position in units of
+ *                 2^-64: round(f_i / (2 pi) * 2^64) mod 2^64.
+ *   rot_dim     : a multiple of 16, at most d (FA_ERR_UNSUPPORTED for another value up to d).
+ *   magnitude   : factor of the rotated elements, finite and > 0 (1 without a scaling that
+ *                 asks for one).
+ * d in {64, 128}, B * N < 2^31 - 256 and at most 65535 heads (FA_ERR_UNSUPPORTED).
+ * Returns FA_ERR_INVALID_ARG for null, misaligned (16 bytes; positions 4, turns 8) or
+ * otherwise bad arguments.
+ */
+FA_API int fa_rope(const void *q, void *q_out, const void *k, void *k_out, int B, int H, int Hk,
+                   int N, int d, const long long *q_strides, const long long *q_out_strides,
+                   const long long *k_strides, const long long *k_out_strides,
+                   const int *positions, int positions_per_batch, const unsigned long long *turns,
+                   int rot_dim, int interleaved, float magnitude, int dtype, void *stream);
+
+/*
+ * Backward pass of fa_rope: the gradients of its inputs from those of its outputs (the
+ * transposed map: the same with sin a negated).  Arguments as fa_rope's.
+ */
+FA_API int fa_rope_bwd(const void *dq_rot, void *dq, const void *dk_rot, void *dk, int B, int H,
+                       int Hk, int N, int d, const long long *dq_rot_strides,
+                       const long long *dq_strides, const long long *dk_rot_strides,
+                       const long long *dk_strides, const int *positions, int positions_per_batch,
+                       const unsigned long long *turns, int rot_dim, int interleaved,
+                       float magnitude, int dtype, void *stream);
+
+/*
+ * Appends a step's new keys and values to a paged cache, rotating keys (and queries) on the
+ * way.  Sequence b holds cache_len[b] tokens; its new token t < new_len[b] goes to slot
+ * cache_len[b] + t, i.e. to row slot % page_size of page block_table[b][slot / page_size]:
+ *     k_cache[page][h][row] = rotated k[b][h][t],  v_cache[page][h][row] = v[b][h][t],
+ *     q_out[b][h][t] = rotated q[b][h][t].
+ * Everything else in the caches, and rows t >= new_len[b] of q_out, stays as it was.  The
+ * lengths are not advanced: the caller does that once the tokens are accepted.
+ *   k, v        : DEVICE [B, Hk, T, d] 16-bit.  q, q_out: DEVICE [B, H, T, d], or both NULL
+ *                 (H is then ignored); q_out may be q.
+ *   k_cache, v_cache : DEVICE [num_pages, Hk, page_size, d], written.
+ *   *_strides   : as fa_rope (caches: page, head, row of a page), NULL for contiguous.
+ *   page_size   : a power of two >= 8 (FA_ERR_UNSUPPORTED otherwise).
+ *   block_table : DEVICE int32 [B, max_blocks].  cache_len: DEVICE int32 [B].
+ *   new_len     : DEVICE int32 [B], or NULL for T each.
+ *   positions   : DEVICE int32 [B, T] (a drafted tree's tokens: cache_len + depth), or NULL
+ *                 for cache_len[b] + t.
+ *   turns, rot_dim, interleaved, magnitude: as fa_rope; turns NULL for no rotation (the
+ *                 other three are then ignored).
+ * A negative length counts as 0, a new_len above T as T.  A token whose slot is behind
+ * max_blocks * page_size, or whose page number is outside [0, num_pages), is not written.
+ * All of these report FA_ERR_BAD_PAGE in the device status word.  Two tokens of one call must not share a slot (a page listed by
+ * two sequences may be shared only where neither writes).  Sizes as fa_rope, with
+ * H + 2 Hk heads; max_blocks * page_size < 2^31 - 256.
+ */
+FA_API int fa_kv_append(const void *k, const void *v, void *k_cache, void *v_cache, const void *q,
+                        void *q_out, int B, int H, int Hk, int T, int d,
+                        const long long *k_strides, const long long *v_strides,
+                        const long long *q_strides, const long long *q_out_strides,
+                        const long long *k_cache_strides, const long long *v_cache_strides,
+                        int num_pages, int page_size, const int *block_table, int max_blocks,
+                        const int *cache_len, const int *new_len, const int *positions,
+                        const unsigned long long *turns, int rot_dim, int interleaved,
+                        float magnitude, int dtype, void *stream);
+
+/*
+ * Attention of a step's new tokens over a paged cache that already holds their keys and
+ * values (fa_kv_append with the same table and lengths): the paged, shared-head counterpart
+ * of fa_fwd_splitkv.  Query head h reads key/value head h / (H / Hk).  New token t of
+ * sequence b (t < new_len[b]) sees key j of its sequence iff
+ *     j < cache_len[b], or  i = j - cache_len[b] < new_len[b]  and
+ *     (tree_mask ? tree_mask[b][t][i] != 0 : i <= t),
+ * so one token, a chain (a prompt's chunk) or a tree of drafted tokens are the same call.
+ *   q, o        : DEVICE [B, H, T, d] 16-bit; *_strides as fa_rope (o not a broadcast).
+ *   lse         : DEVICE [B, H, T] fp32, contiguous.
+ *   k_cache .. new_len : as fa_kv_append (read only).
+ *   tree_mask   : DEVICE uint8 [T, T] (tree_per_batch = 0) or [B, T, T] (1), row = token,
+ *                 column = key; NULL for a chain.  Rows and columns from new_len[b] on are
+ *                 not read.
+ *   workspace   : DEVICE scratch of fa_fwd_paged_workspace_bytes(B, H, Hk, T, d) bytes,
+ *                 256-byte aligned, contents irrelevant and clobbered; it must not be shared
+ *                 by calls that may run at the same time.  The size depends on the current
+ *                 device: call both on the same one.
+ * Rows that see no key, rows t >= new_len[b] among them, get O = 0, LSE = -inf.  Slots from
+ * cache_len[b] + new_len[b] on are never used, whatever they hold; keys that a row's mask
+ * hides do not touch that row either, infinities and NaN in them included.  Lengths are
+ * clamped to 0 <= cache_len <= max_blocks * page_size, 0 <= new_len <= T and a sum within the
+ * table; page numbers outside [0, num_pages) make their keys invisible; both report
+ * FA_ERR_BAD_PAGE in the device status word.
+ * H must be a multiple of Hk.  Returns FA_ERR_INVALID_ARG for bad arguments or a missing,
+ * small or misaligned workspace, FA_ERR_UNSUPPORTED for sizes beyond fa_rope's or when
+ * ceil(T * H / Hk / 32) * Hk * max_blocks * page_size / 128 reaches 2^31.  Forward only.
+ */
+FA_API size_t fa_fwd_paged_workspace_bytes(int B, int H, int Hk, int T, int d);
+
+FA_API int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *o,
+                        float *lse, int B, int H, int Hk, int T, int d, const long long *q_strides,
+                        const long long *o_strides, const long long *k_cache_strides,
+                        const long long *v_cache_strides, int num_pages, int page_size,
+                        const int *block_table, int max_blocks, const int *cache_len,
+                        const int *new_len, const unsigned char *tree_mask, int tree_per_batch,
+                        float scale, int dtype, void *workspace, size_t workspace_bytes,
+                        void *stream);
 
 /*
  * Optional timing hook for profiling.  After this call, every launch made by this host
