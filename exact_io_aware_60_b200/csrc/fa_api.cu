@@ -808,38 +808,74 @@ bool make_cache_map(CUtensorMap *m, const fa::Rows &r, int bf16, int d, int page
     return true;
 }
 
-// Rows of a tile: the copies of the rows (REP) that fit 128 lanes.
-int paged_rows(long long R) { return R <= 32 ? 32 : (R <= 64 ? 64 : 128); }
+// How an item's rows are laid out (see PagedParams).
+struct PagedShape {
+    int rows;   // of an item: 32, 64, 128 (copies: 4, 2, 1) or 256 (two row tiles)
+    int GP, GT, TPT;
+    long long row_tiles;
+};
+PagedShape paged_shape(int G, int T) {
+    PagedShape s;
+    s.GT = (G + 127) / 128;
+    s.GP = (G + s.GT - 1) / s.GT;
+    const long long R = (long long)T * s.GP;
+    s.rows = R <= 32 ? 32 : (R <= 64 ? 64 : (R <= 128 ? 128 : 256));
+    s.TPT = std::min(s.rows, 128) / s.GP;
+    const int per = s.TPT * (s.rows == 256 ? 2 : 1);
+    s.row_tiles = ((long long)T + per - 1) / per * s.GT;
+    return s;
+}
 
 struct PagedWorkspace {
     size_t o_bytes, total;
 };
-PagedWorkspace paged_workspace(long long R, int d, int ctas) {
-    const size_t rows = (size_t)2 * ctas * paged_rows(R);
+PagedWorkspace paged_workspace(int rows, int d, int ctas) {
+    const size_t n = (size_t)2 * ctas * rows;
     PagedWorkspace w;
-    w.o_bytes = round256(rows * d * 4);
-    w.total = w.o_bytes + round256(rows * 4);
+    w.o_bytes = round256(n * d * 4);
+    w.total = w.o_bytes + round256(n * 4);
     return w;
 }
 
-template <int D, bool BF16, int REP>
-int launch_paged(const CUtensorMap &mk, const CUtensorMap &mv, const fa::PagedParams &p, int cap_tiles,
-                 cudaStream_t st, int dev) {
-    using C = fa::PagedCfg<D>;
-    auto kern = fa::fa_paged_kernel<D, BF16, REP>;
+// 4-D view [B][T][H][d] of the queries; box = one row tile.
+bool make_query_map(CUtensorMap *m, const fa::Rows &r, int bf16, int d, int H, int T, int B, int GP,
+                    int TPT) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+    const long long s[3] = {H > 1 ? r.sh : d, T > 1 ? r.st : d, B > 1 ? r.sb : d};
+    cuuint64_t strides[3] = {(cuuint64_t)(s[0] * 2), (cuuint64_t)(s[1] * 2), (cuuint64_t)(s[2] * 2)};
+    cuuint32_t box[4] = {64, (cuuint32_t)GP, (cuuint32_t)TPT, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult e = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                     const_cast<uint16_t *>(r.p), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (e != CUDA_SUCCESS) {
+        snprintf(t_last_error, sizeof(t_last_error), "cuTensorMapEncodeTiled failed (%d)", (int)e);
+        return false;
+    }
+    return true;
+}
+
+template <int D, bool BF16, int REP, int RT>
+int launch_paged(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                 const fa::PagedParams &p, int cap_tiles, cudaStream_t st, int dev) {
+    using C = fa::PagedCfg<D, REP, RT>;
+    auto kern = fa::fa_paged_kernel<D, BF16, REP, RT>;
     static std::atomic<int> smem_done[kMaxDevices];
     cudaError_t e = set_smem(kern, C::SMEM, smem_done, dev);
     if (e != cudaSuccess) {
         record_cuda_error(e, "cudaFuncSetAttribute(paged)");
         return FA_ERR_CUDA;
     }
-    constexpr int ROWS = 128 / REP;
-    e = launch_pdl(kern, dim3((unsigned)p.ctas), dim3(C::THREADS), C::SMEM, st, mk, mv, p);
+    e = launch_pdl(kern, dim3((unsigned)p.ctas), dim3(C::THREADS), C::SMEM, st, mq, mk, mv, p);
     if (e == cudaSuccess && cap_tiles > 1) {
-        const int rows = std::min((long long)ROWS, (long long)p.T * p.G);
-        e = launch_pdl(fa::fa_paged_merge_kernel<D, BF16>,
+        // rows in use: all of an item's, or those of the call's tokens where these are fewer
+        const int rows = RT == 2 ? 256 : std::min(p.TPT, p.T) * p.GP;
+        e = launch_pdl(fa::fa_paged_merge_kernel<D, BF16, RT>,
                        dim3((unsigned)(p.B * p.Hk * p.row_tiles), (unsigned)((rows + 3) / 4)),
-                       dim3(128), 0, st, p, (int)ROWS);
+                       dim3(128), 0, st, p, (int)C::ROWS);
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
@@ -1246,7 +1282,7 @@ int fa_kv_append(const void *k, const void *v, void *k_cache, void *v_cache, con
 
 size_t fa_fwd_paged_workspace_bytes(int B, int H, int Hk, int T, int d) {
     if (B < 1 || Hk < 1 || H < Hk || H % Hk != 0 || T < 1 || (d != 64 && d != 128)) return 0;
-    return paged_workspace((long long)T * (H / Hk), d, current_sms()).total;
+    return paged_workspace(paged_shape(H / Hk, T).rows, d, current_sms()).total;
 }
 
 int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *o, float *lse, int B,
@@ -1270,25 +1306,23 @@ int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *
     rc = make_pages(&p.pt, num_pages, page_size, block_table, max_blocks, cache_len, new_len);
     if (rc != FA_OK) return rc;
     if ((double)num_pages * Hk * page_size * d > (double)FA_MAX_ELEMENTS) return FA_ERR_UNSUPPORTED;
-    fa::Rows kc;
-    if (!make_rows(&p.q, q, q_strides, B, H, T, d, true) || !make_rows(&p.o, o, o_strides, B, H, T, d, false) ||
+    fa::Rows qr, kc;
+    if (!make_rows(&qr, q, q_strides, B, H, T, d, false) || !make_rows(&p.o, o, o_strides, B, H, T, d, false) ||
         !make_rows(&kc, k_cache, k_cache_strides, num_pages, Hk, page_size, d, false) ||
         !make_rows(&p.vc, v_cache, v_cache_strides, num_pages, Hk, page_size, d, false))
         return FA_ERR_INVALID_ARG;
     const int G = H / Hk;
-    const long long R = (long long)T * G;
-    const int rows = paged_rows(R);
-    const long long row_tiles = (R + rows - 1) / rows;
+    const PagedShape sh = paged_shape(G, T);
     const long long cap_tiles = ((long long)max_blocks * page_size + 127) / 128;
     // units of one sequence and items of the call are counted in 32 bits
-    if (R >= (1LL << 31) - 256 || row_tiles * Hk * std::max(cap_tiles, 1LL) >= (1LL << 31) ||
-        row_tiles * Hk * B >= (1LL << 31))
+    if ((double)sh.row_tiles * Hk * cap_tiles >= (double)(1LL << 31) ||
+        (double)sh.row_tiles * Hk * B >= (double)(1LL << 31))
         return FA_ERR_UNSUPPORTED;
     int dev = 0;
     rc = check_device(&dev);
     if (rc != FA_OK) return rc;
     const int ctas = current_sms();
-    const PagedWorkspace ws = paged_workspace(R, d, ctas);
+    const PagedWorkspace ws = paged_workspace(sh.rows, d, ctas);
     if (!workspace || workspace_bytes < ws.total || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return FA_ERR_INVALID_ARG;
     p.lse = lse;
@@ -1300,22 +1334,29 @@ int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *
     p.Hk = Hk;
     p.G = G;
     p.T = T;
-    p.row_tiles = (int)row_tiles;
-    p.ctas = (int)std::min<long long>(ctas, row_tiles * Hk * B * std::max(cap_tiles, 1LL));
+    p.GP = sh.GP;
+    p.GT = sh.GT;
+    p.TPT = sh.TPT;
+    p.row_tiles = (int)sh.row_tiles;
+    p.ctas = (int)std::min<double>(ctas, (double)sh.row_tiles * Hk * B * cap_tiles);
     p.scale_log2 = scale * 1.4426950408889634f;
     const bool bf16 = dtype == FA_BF16;
-    CUtensorMap mk, mv;
+    CUtensorMap mq, mk, mv;
     const int box_rows = std::min(page_size, 128);
-    if (!make_cache_map(&mk, kc, bf16, d, page_size, Hk, num_pages, box_rows) ||
+    if (!make_query_map(&mq, qr, bf16, d, H, T, B, sh.GP, sh.TPT) ||
+        !make_cache_map(&mk, kc, bf16, d, page_size, Hk, num_pages, box_rows) ||
         !make_cache_map(&mv, p.vc, bf16, d, page_size, Hk, num_pages, box_rows))
         return FA_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-#define FA_PAGED(D, BF) (rows == 32 ? launch_paged<D, BF, 4>(mk, mv, p, (int)cap_tiles, st, dev) \
-                         : rows == 64 ? launch_paged<D, BF, 2>(mk, mv, p, (int)cap_tiles, st, dev) \
-                                      : launch_paged<D, BF, 1>(mk, mv, p, (int)cap_tiles, st, dev))
+#define FA_PAGED_ARGS mq, mk, mv, p, (int)cap_tiles, st, dev
+#define FA_PAGED(D, BF) (sh.rows == 32    ? launch_paged<D, BF, 4, 1>(FA_PAGED_ARGS) \
+                         : sh.rows == 64  ? launch_paged<D, BF, 2, 1>(FA_PAGED_ARGS) \
+                         : sh.rows == 128 ? launch_paged<D, BF, 1, 1>(FA_PAGED_ARGS) \
+                                          : launch_paged<D, BF, 1, 2>(FA_PAGED_ARGS))
     if (d == 64) return bf16 ? FA_PAGED(64, true) : FA_PAGED(64, false);
     return bf16 ? FA_PAGED(128, true) : FA_PAGED(128, false);
 #undef FA_PAGED
+#undef FA_PAGED_ARGS
 }
 
 }  // extern "C"

@@ -2,9 +2,9 @@
 //
 // Sequence b holds cache_len[b] tokens and new_len[b] new ones (one token, a chain or a tree
 // of drafted tokens), all in the cache's pages.  New token t of b sees every held key and the
-// new keys its mask row names (chain: keys up to itself).  With G query heads to a key/value
-// head, the R = T * G rows that share a key/value head are packed into tiles of 128 rows
-// (row r = token r / G, head r % G), so that the cache is read once for all of them:
+// new keys its mask row names (chain: keys up to itself).  The G query heads of a key/value
+// head are packed with the tokens into tiles of ROWS rows (row r = token r / G, head r % G),
+// so that the cache is read once for all of them:
 //   S = Q K^T on tcgen05 (M = 128 rows, 128 keys), online softmax with a running maximum m
 //   and sum l per row, O += P V.
 //
@@ -18,14 +18,15 @@
 // cut item go to the workspace as fp32 (normalised O, log-sum-exp) and a second kernel,
 // launched early by PDL, merges them in a fixed order.
 //
-// CTA: warps 0..3 softmax (one row per thread), warp 4 producer (page table and TMA), warp 5
-// MMA issuer, warp 6 loads Q and repairs V tiles with slots behind the sequence's end (their
-// contents are unspecified, and 0 * NaN would reach O).
+// CTA: softmax warps (one row per thread, 4 per row tile), then one producer warp (page table
+// and TMA of K and V), one MMA issuer, and one that loads Q and repairs V tiles (see repair).
 //
 // Few rows (REP = 4: a tile of 32 rows, REP = 2: 64): the rows are repeated in the tile's
 // REP lane quarters / halves, and each copy takes 1 / REP of the keys of every tile as a
 // softmax of its own (P is zero elsewhere); the copies are merged in the epilogue.  The
 // exponentials of a tile then take 1 / REP of the time.
+// Many rows (RT = 2): two tiles of 128 rows share every K and V tile, each with softmax warps
+// of its own, so that one tile's products run beside the other's exponentials.
 #pragma once
 
 #include <cuda.h>
@@ -36,68 +37,88 @@
 namespace fa {
 
 struct PagedParams {
-    Rows q, o;           // [B, H, T, d]
+    Rows o;              // [B, H, T, d]
     Rows vc;             // the value cache (also behind the tensor map)
     float *lse;          // [B, H, T]
     PageTable pt;
     const uint8_t *tree; // [B or 1, T, T], nullptr: chain
     long long tree_sb;   // bytes between sequences (0: shared)
-    float *part_o;       // [2 * gridDim.x][rows of a tile][D]
-    float *part_lse;     // [2 * gridDim.x][rows of a tile], base 2
+    float *part_o;       // [2 * gridDim.x][rows of an item][D]
+    float *part_lse;     // [2 * gridDim.x][rows of an item], base 2
     int B, Hk, G, T;
-    int row_tiles;       // tiles of an item's R rows
+    int GP, GT;          // heads of a row tile; row tiles that a token's G heads take (1 up to
+                         // 128 heads to a key/value head)
+    int TPT;             // tokens of a row tile: (rows of a tile) / GP
+    int row_tiles;       // items of a (sequence, key/value head): ceil(T / (TPT * RT)) * GT
     int ctas;            // shares
     float scale_log2;
 };
 
-template <int D>
+template <int D, int REP, int RT>
 struct PagedCfg {
+    static_assert(REP == 1 || RT == 1, "copies of one row tile, or two row tiles");
     static constexpr int BN = 128;              // keys per tile
+    static constexpr int ROWS = 128 / REP;      // rows of a row tile
     static constexpr int HALVES = D / 64;
     static constexpr int QTILE = 128 * D * 2;
     static constexpr int TILE = BN * D * 2;     // K or V tile
     static constexpr int HALF = BN * 128;       // one 64-element column block of a tile
-    static constexpr int NS = (D == 64) ? 11 : 5;  // ring of K and V tiles, alternating
-    static constexpr int MERGE = 4 * 32 * 33 * 4;  // REP merge: a padded 32 x 32 block per warp
+    static constexpr int NS = (D == 64) ? (RT == 1 ? 11 : 10) : (RT == 1 ? 5 : 4);  // K, V ring
+    // REP merge: a 32-column block of every row and copy, rows padded to 36 columns
+    static constexpr int MERGE = (REP > 1) ? 128 * 36 * 4 : 0;
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_RING = OFF_Q + QTILE;
+    static constexpr int OFF_RING = OFF_Q + RT * QTILE;
     static constexpr int OFF_MERGE = OFF_RING + NS * TILE;
     static constexpr int OFF_BAR = OFF_MERGE + MERGE;
     static constexpr int USED = OFF_BAR + 2560;
     static constexpr int SMEM = USED + 1024;
-    static constexpr int THREADS = 224;
-    static constexpr uint32_t COL_S = 0;        // two score buffers
-    static constexpr uint32_t COL_P = 256;      // two P buffers of 64 columns
-    static constexpr uint32_t COL_O = 384;
-    static_assert(COL_O + D <= 512, "TMEM budget");
+    static constexpr int SOFT = 4 * RT;         // softmax warps
+    // (two row tiles: whole warpgroups, so that registers can move from the other four warps
+    // to the softmax: 384 x 168 = 64512 at launch = 256 x 216 + 128 x 72)
+    static constexpr int THREADS = RT == 1 ? 224 : 384;
+    // TMEM: two score buffers (RT = 1: alternating tiles; RT = 2: one per row tile).  P has
+    // columns of its own except at d = 128 with two row tiles, where it overwrites S.
+    static constexpr bool P_OWN = !(D == 128 && RT == 2);
+    static constexpr uint32_t COL_S = 0;
+    static constexpr uint32_t COL_P = P_OWN ? 256 : 0;
+    static constexpr uint32_t P_STEP = P_OWN ? 64 : 128;
+    static constexpr uint32_t COL_O = P_OWN ? 384 : 256;
+    static_assert(COL_O + RT * D <= 512, "TMEM budget");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 struct PagedBars {
     uint64_t q_full, q_empty, o_empty;
+    // The MMA issuer asks for the repair of a tile's V once the tile's S is issued: from then
+    // on the V slot's fill is the next or the last one, so that the parity that the repairing
+    // warp waits for is unambiguous.  (Two, alternating: a request may be made while the one
+    // before it is not yet served.)
+    uint64_t need[2];
+    // index: RT = 1 the tile's parity, RT = 2 the row tile
     uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
-    uint64_t full[12], empty[12], fixed[12];  // per ring slot; fixed: V repaired by warp 6
+    uint64_t full[12], empty[12], fixed[12];  // per ring slot; fixed: V repaired
     uint32_t tmem_base;
     int b0;                 // this CTA's share: first sequence, its first unit, the share
     long long base0, u0, u1;
     uint32_t bad[16];       // per tile: sub-pages whose page number is outside the cache
-    // Item t & 3 hides keys whose V is not finite.  (Four: warp 6 reaches item t + 4 only
-    // after the softmax of item t + 1 began.)
+    // Item t & 3 hides keys whose V is not finite.  (Four: the repairing warp reaches item
+    // t + 4 only after the softmax of item t + 1 began.)
     int poison[4];
     float stat[3][128];     // REP merge: m, l, l of the rounded weights
 };
 
-// Work units of a sequence: `tiles` per (head, row tile with new tokens), one for a row tile
-// without (its rows are written as empty).
+// Work units of a sequence: `tiles` per (head, item with new tokens), one for an item without
+// (its rows are written as empty).
 struct PagedSeq {
-    int past, fresh, tiles, valid;  // valid: row tiles that hold a new token
+    int past, fresh, tiles, valid;  // valid: items that hold a new token
     int per_head;
 };
-__device__ __forceinline__ PagedSeq paged_seq(const PagedParams &p, int rows, int b) {
+template <int RT>
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams &p, int b) {
     PagedSeq s;
     page_lengths(p.pt, p.T, b, s.past, s.fresh);
     s.tiles = (s.past + s.fresh + 127) >> 7;
-    s.valid = (int)(((long long)s.fresh * p.G + rows - 1) / rows);
+    s.valid = (s.fresh + p.TPT * RT - 1) / (p.TPT * RT) * p.GT;
     s.per_head = s.valid * s.tiles + (p.row_tiles - s.valid);
     return s;
 }
@@ -108,15 +129,17 @@ __device__ __forceinline__ long long warp_sum(long long v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-__device__ __forceinline__ long long paged_units(const PagedParams &p, int rows, int lane, int upto) {
+template <int RT>
+__device__ __forceinline__ long long paged_units(const PagedParams &p, int lane, int upto) {
     long long n = 0;
-    for (int b = lane; b < upto; b += 32) n += (long long)paged_seq(p, rows, b).per_head * p.Hk;
+    for (int b = lane; b < upto; b += 32) n += (long long)paged_seq<RT>(p, b).per_head * p.Hk;
     return warp_sum(n);
 }
 
 // One piece of work: key tiles [j0, j1) of one item.
 struct PagedSeg {
-    int b, hk, rt;      // sequence, key/value head, row tile
+    int b, hk;          // sequence, key/value head
+    int tok0, g0;       // first token of the rows, first of its heads
     int past, total;    // keys held, keys with the new ones
     int fresh;
     int j0, j1;
@@ -141,23 +164,24 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
     return __vcmpeq2(w & e, e);
 }
 
+template <int RT>
 struct PagedWalk {
     long long u, u1, base;
     int b, index;
     PagedSeq s;
-    __device__ __forceinline__ void init(const PagedParams &p, int rows, const PagedBars *bars) {
+    __device__ __forceinline__ void init(const PagedParams &p, const PagedBars *bars) {
         u = bars->u0;
         u1 = bars->u1;
         b = bars->b0;
         base = bars->base0;
         index = 0;
-        if (u < u1) s = paged_seq(p, rows, b);
+        if (u < u1) s = paged_seq<RT>(p, b);
     }
-    __device__ __forceinline__ bool next(const PagedParams &p, int rows, PagedSeg &g) {
+    __device__ __forceinline__ bool next(const PagedParams &p, PagedSeg &g) {
         if (u >= u1) return false;
         while (u >= base + (long long)s.per_head * p.Hk) {
             base += (long long)s.per_head * p.Hk;
-            s = paged_seq(p, rows, ++b);
+            s = paged_seq<RT>(p, ++b);
         }
         const unsigned r0 = (unsigned)(u - base);
         g.hk = (int)(r0 / (unsigned)s.per_head);
@@ -167,23 +191,25 @@ struct PagedWalk {
         g.fresh = s.fresh;
         g.total = s.past + s.fresh;
         g.index = index++;
+        int rt;
         if (r < s.valid * s.tiles) {
-            g.rt = r / s.tiles;
-            g.j0 = r - g.rt * s.tiles;
+            rt = (int)((unsigned)r / (unsigned)s.tiles);
+            g.j0 = r - rt * s.tiles;
             const long long left = u1 - u;
             g.j1 = (int)min((long long)s.tiles, g.j0 + left);
             u += g.j1 - g.j0;
             g.whole = g.j0 == 0 && g.j1 == s.tiles;
-            if (p.tree == nullptr) {  // a chain's rows see no key behind their last token
-                const int t1 = min(s.fresh, (g.rt * rows + rows - 1) / p.G + 1);
-                g.j1 = min(g.j1, (s.past + t1 + 127) >> 7);
-            }
         } else {
-            g.rt = s.valid + (r - s.valid * s.tiles);
+            rt = s.valid + (r - s.valid * s.tiles);
             g.j0 = g.j1 = 0;
             g.whole = true;
             u += 1;
         }
+        const int tt = p.GT == 1 ? rt : rt / p.GT;
+        g.tok0 = tt * RT * p.TPT;
+        g.g0 = p.GT == 1 ? 0 : (rt - tt * p.GT) * p.GP;
+        if (p.tree == nullptr)  // a chain's rows see no key behind their last token
+            g.j1 = min(g.j1, (s.past + min(s.fresh, g.tok0 + RT * p.TPT) + 127) >> 7);
         return true;
     }
 };
@@ -197,14 +223,6 @@ __device__ __forceinline__ void tma_load_4d(void *smem_dst, const void *tmap, ui
         : "memory");
 }
 
-// 16 bytes global -> shared, asynchronous; zeros where !valid.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(valid ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // C columns of 32 TMEM lanes.
 template <int C>
 __device__ __forceinline__ void tmem_ldn(uint32_t a, uint32_t (&r)[C]) {
@@ -213,13 +231,34 @@ __device__ __forceinline__ void tmem_ldn(uint32_t a, uint32_t (&r)[C]) {
     else tmem_ld32(a, r);
 }
 
-template <int D, bool BF16, int REP>
-__global__ void __launch_bounds__(224, 1)
-fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                const __grid_constant__ PagedParams p) {
-    using C = PagedCfg<D>;
-    constexpr int ROWS = 128 / REP;   // rows of a tile
+// Two fp32 operations at once (packed registers).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+template <int D, bool BF16, int REP, int RT>
+__global__ void __launch_bounds__(PagedCfg<D, REP, RT>::THREADS, 1)
+fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedParams p) {
+    using C = PagedCfg<D, REP, RT>;
+    constexpr int ROWS = C::ROWS;
     constexpr int CW = 128 / REP;     // keys of a tile that one thread handles
+    constexpr int W_TMA = C::SOFT, W_MMA = C::SOFT + 1, W_FIX = C::SOFT + 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sQ = smem + C::OFF_Q;
@@ -229,13 +268,21 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 160) {
+    // Barrier index and phase of tile g (RT = 1: two alternating buffers; RT = 2: row tile i
+    // has one).
+    auto bi = [](int g, int i) { return RT == 1 ? (g & 1) : i; };
+    auto ph = [](int g) { return RT == 1 ? ((g >> 1) & 1) : (g & 1); };
+    constexpr int BUFS = RT == 1 ? 2 : 1;  // tiles between two uses of a buffer
+
+    if (threadIdx.x == W_MMA * 32) {
+        tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
         mbar_init(&bars->q_full, 1);
         mbar_init(&bars->q_empty, 1);
-        mbar_init(&bars->o_empty, 128);
+        mbar_init(&bars->o_empty, 128 * RT);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->need[i], 1);
             mbar_init(&bars->s_full[i], 1);
             mbar_init(&bars->s_empty[i], 128);
             mbar_init(&bars->p_full[i], 128);
@@ -248,14 +295,14 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         fence_mbar_init();
     }
-    if (warp == 6) tmem_alloc(&bars->tmem_base, 512);
+    if (warp == W_FIX) tmem_alloc(&bars->tmem_base, 512);
     pdl_wait();
     pdl_launch_dependents();
-    if (warp == 4) {
+    if (warp == W_TMA) {
         if (blockIdx.x == 0)
             for (int b = lane; b < p.B; b += 32) page_lengths_check(p.pt, p.T, b);
         // this CTA's share of the units
-        const long long W = paged_units(p, ROWS, lane, p.B);
+        const long long W = paged_units<RT>(p, lane, p.B);
         const long long G = min((long long)p.ctas, W);
         const long long c = blockIdx.x;
         const long long u0 = c < G ? c * W / G : 0, u1 = c < G ? (c + 1) * W / G : 0;
@@ -265,7 +312,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (u0 < u1) {
             for (int k = 0; k < p.B; k += 32) {
                 const long long mine =
-                    k + lane < p.B ? (long long)paged_seq(p, ROWS, k + lane).per_head * p.Hk : 0;
+                    k + lane < p.B ? (long long)paged_seq<RT>(p, k + lane).per_head * p.Hk : 0;
                 long long upto = mine;  // inclusive prefix sum
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -294,12 +341,13 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
 
-    PagedWalk walk;
-    walk.init(p, ROWS, bars);
+    PagedWalk<RT> walk;
+    walk.init(p, bars);
     PagedSeg it;
 
-    if (warp == 4) {
-        // ------------------------------ producer: whole warp ---------------------------
+    if (warp == W_TMA) {
+        // ------------------------------ K and V: whole warp -----------------------------
+        if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // A tile's pages: npt boxes (a page, or 128 rows of a larger one) per 64-element
         // column block; lane l loads box l % npt of block l / npt.
         const int page = 1 << p.pt.page_shift;
@@ -308,7 +356,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         const int mine = lane % npt, half = lane / npt;
         int gj = 0;  // tiles so far
         bool ok = true;
-        while (ok && walk.next(p, ROWS, it)) {
+        while (ok && walk.next(p, it)) {
             const int *row = p.pt.table + (long long)it.b * p.pt.max_blocks;
             for (int j = it.j0; j < it.j1; ++j, ++gj) {
                 const int key = j * 128 + mine * box_rows;
@@ -343,100 +391,117 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (!ok)  // a wait gave up: the copies in flight land before the CTA's memory goes
             for (int n = max(0, 2 * gj + 1 - C::NS); n < 2 * gj + 2; ++n)
                 (void)mbar_wait(&bars->full[n % C::NS], (n / C::NS) & 1);
-    } else if (warp == 5) {
+    } else if (warp == W_MMA) {
         // ------------------------------ MMA issuer --------------------------------------
+        if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (lane == 0) {
             constexpr uint32_t kIdescS = idesc_f16(BF16, false, false, 128, 128);
             constexpr uint32_t kIdescO = idesc_f16(BF16, false, true, 128, D);
             const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
             const uint64_t k_desc = smem_desc_sw128(smem_u32(ring), 16, 1024);
             const uint64_t v_desc = smem_desc_sw128(smem_u32(ring), C::HALF, 1024);
-            auto issue_s = [&](int g) -> bool {
+            int asked = 0;
+            // S of tile g (key tile j), row tile i (K's slot is released by the last row tile's)
+            auto issue_s = [&](int g, int i, int j) -> bool {
                 const int n = 2 * g, s = n % C::NS;
                 if (!mbar_wait(&bars->full[s], (n / C::NS) & 1)) return false;
-                if (g >= 2 && !mbar_wait(&bars->s_empty[g & 1], (g / 2 - 1) & 1)) return false;
+                if (g >= BUFS && !mbar_wait(&bars->s_empty[bi(g, i)], ph(g - BUFS))) return false;
                 tc_fence_after();
                 const uint64_t kd = k_desc + (uint64_t)((s * C::TILE) >> 4);
+                const uint64_t qd = q_desc + (uint64_t)((i * C::QTILE) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint64_t qo = (uint64_t)(((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4);
                     const uint64_t ko = (uint64_t)(((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4);
-                    mma_ss(tmem + C::COL_S + (g & 1) * 128, q_desc + qo, kd + ko, kIdescS, kk > 0);
+                    mma_ss(tmem + C::COL_S + bi(g, i) * 128, qd + qo, kd + ko, kIdescS, kk > 0);
                 }
-                mma_commit(&bars->empty[s]);
-                mma_commit(&bars->s_full[g & 1]);
+                if (i == RT - 1) mma_commit(&bars->empty[s]);
+                mma_commit(&bars->s_full[bi(g, i)]);
+                if (i == 0 && it.repair(p, j)) mbar_arrive(&bars->need[asked++ & 1]);
                 return true;
+            };
+            // P V of tile g, row tile i
+            auto issue_pv = [&](int g, int i, int s, bool first) {
+                tc_fence_after();
+                const uint64_t vd = v_desc + (uint64_t)((s * C::TILE) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ts(tmem + C::COL_O + i * D, tmem + C::COL_P + bi(g, i) * C::P_STEP + kk * 8,
+                           vd + (uint64_t)((kk * 16 * 128) >> 4), kIdescO, !first || kk > 0);
+                if (i == RT - 1) mma_commit(&bars->empty[s]);
+                mma_commit(&bars->pv_done[bi(g, i)]);
             };
             bool ok = true;
             int gj = 0, t = 0;
             uint32_t fixes = 0;  // parity of each slot's next repair
-            while (ok && walk.next(p, ROWS, it)) {
+            while (ok && walk.next(p, it)) {
                 const int nt = it.j1 - it.j0;
                 if (nt <= 0) continue;
                 if (!mbar_wait(&bars->q_full, t & 1)) break;
                 tc_fence_after();
-                if (!issue_s(gj)) break;
-                for (int i = 0; i < nt; ++i) {
-                    const int g = gj + i;
-                    if (i + 1 < nt) {
-                        if (!issue_s(g + 1)) { ok = false; break; }
-                    } else {
-                        mma_commit(&bars->q_empty);
-                    }
+                for (int i = 0; ok && i < RT; ++i) ok = issue_s(gj, i, it.j0);
+                for (int x = 0; ok && x < nt; ++x) {
+                    const int g = gj + x;
                     const int n = 2 * g + 1, s = n % C::NS;
-                    if (!mbar_wait(&bars->p_full[g & 1], (g / 2) & 1) ||
-                        !mbar_wait(&bars->full[s], (n / C::NS) & 1)) { ok = false; break; }
-                    if (it.repair(p, it.j0 + i)) {
-                        if (!mbar_wait(&bars->fixed[s], (fixes >> s) & 1)) { ok = false; break; }
-                        fixes ^= 1u << s;
-                    }
-                    if (i == 0 && t > 0 && !mbar_wait(&bars->o_empty, (t - 1) & 1)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint64_t vd = v_desc + (uint64_t)((s * C::TILE) >> 4);
+                    const bool more = x + 1 < nt;
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_ts(tmem + C::COL_O, tmem + C::COL_P + (g & 1) * 64 + kk * 8,
-                               vd + (uint64_t)((kk * 16 * 128) >> 4), kIdescO, i > 0 || kk > 0);
-                    mma_commit(&bars->empty[s]);
-                    mma_commit(&bars->pv_done[g & 1]);
+                    for (int i = 0; i < RT; ++i) {
+                        // the next tile's S first where its buffer is another one or is read
+                        // before P is written; behind P V where P overwrites S
+                        if (C::P_OWN && more && !issue_s(g + 1, i, it.j0 + x + 1)) { ok = false; break; }
+                        if (!more && i == RT - 1 && C::P_OWN) mma_commit(&bars->q_empty);
+                        if (!mbar_wait(&bars->p_full[bi(g, i)], ph(g))) { ok = false; break; }
+                        if (i == 0) {
+                            if (!mbar_wait(&bars->full[s], (n / C::NS) & 1)) { ok = false; break; }
+                            if (it.repair(p, it.j0 + x)) {
+                                if (!mbar_wait(&bars->fixed[s], (fixes >> s) & 1)) { ok = false; break; }
+                                fixes ^= 1u << s;
+                            }
+                            if (x == 0 && t > 0 && !mbar_wait(&bars->o_empty, (t - 1) & 1)) {
+                                ok = false;
+                                break;
+                            }
+                        }
+                        issue_pv(g, i, s, x == 0);
+                        if (!C::P_OWN && more && !issue_s(g + 1, i, it.j0 + x + 1)) { ok = false; break; }
+                        if (!more && i == RT - 1 && !C::P_OWN) mma_commit(&bars->q_empty);
+                    }
                 }
                 gj += nt;
                 ++t;
             }
         }
-    } else if (warp == 6) {
-        // ------------------------------ Q loads, V tails --------------------------------
+    } else if (warp == W_FIX) {
+        // ------------------------------ Q loads, V repairs ------------------------------
+        if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         bool ok = true;
-        int gj = 0, t = 0;
-        while (ok && walk.next(p, ROWS, it)) {
+        int gj = 0, t = 0, served = 0;
+        while (ok && walk.next(p, it)) {
             const int nt = it.j1 - it.j0;
             if (nt <= 0) continue;
             if (t > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (t - 1) & 1))) break;
-            constexpr int CH = D / 8;        // 16-byte chunks of a row
-            constexpr int RPI = 32 / CH;     // rows per step
-            const int ch = lane % CH;
-            const long long qb = it.b * p.q.sb;
-            for (int i = lane / CH; i < 128; i += RPI) {
-                const int r = it.rt * ROWS + (i % ROWS);
-                const int tok = r / p.G, h = it.hk * p.G + (r - tok * p.G);
-                const bool valid = tok < it.fresh;
-                const uint16_t *src = p.q.p + (valid ? qb + h * p.q.sh + tok * p.q.st : 0) + ch * 8;
-                const uint32_t dst = smem_u32(sQ) + (ch >> 3) * (128 * 128) + i * 128 +
-                                     (((ch & 7) ^ (i & 7)) << 4);
-                cp_async16(dst, src, valid);
+            if (lane == 0) {
+                // a box of TPT tokens x GP heads is a row tile (zeros behind the last token)
+                mbar_arrive_expect_tx(&bars->q_full, p.TPT * p.GP * 128 * C::HALVES * REP * RT);
+#pragma unroll
+                for (int i = 0; i < RT * REP; ++i)
+#pragma unroll
+                    for (int hf = 0; hf < C::HALVES; ++hf)
+                        tma_load_4d(sQ + (RT > 1 ? i * C::QTILE : i * ROWS * 128) + hf * (128 * 128), &tmQ,
+                                    &bars->q_full, hf * 64, it.hk * p.G + it.g0,
+                                    it.tok0 + (RT > 1 ? i * p.TPT : 0), it.b);
             }
-            cp_async_wait_all();
-            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->q_full);
             // V tiles with new keys or slots behind them
             bool found = false;
             for (int i = 0; ok && i < nt; ++i) {
                 const int j = it.j0 + i;
                 if (!it.repair(p, j)) continue;
                 const int n = 2 * (gj + i) + 1, s = n % C::NS;
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars->full[s], (n / C::NS) & 1));
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->need[served & 1], (served >> 1) & 1) &&
+                                                 mbar_wait(&bars->full[s], (n / C::NS) & 1));
                 if (!ok) break;
+                ++served;
                 // (the swizzle permutes 16-byte chunks within a row only)
                 uint8_t *tile = ring + s * C::TILE;
                 const int tail = min(128, it.total - j * 128);
@@ -471,14 +536,20 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             ++t;
             gj += nt;
         }
-    } else {
+        // the last Q load has landed before the CTA's memory goes (at once unless a wait gave up)
+        if (t > 0) (void)mbar_wait(&bars->q_full, (t - 1) & 1);
+    } else if (warp < C::SOFT) {
         // ------------------------------ softmax warps -----------------------------------
+        if constexpr (RT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         constexpr int WPC = 4 / REP;                       // warps of one copy of the rows
-        const int row = (warp % WPC) * 32 + lane;          // row of the tile
-        const int kw = warp / WPC;                         // the copy: keys [kw * CW, + CW)
-        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-        const uint32_t ob = tmem + lane_base + C::COL_O;
+        const int ti = RT == 1 ? 0 : warp >> 2;            // row tile
+        const int wq = warp & 3;                           // lane quarter of TMEM
+        const int row = (wq % WPC) * 32 + lane;            // row of the tile
+        const int kw = wq / WPC;                           // the copy: keys [kw * CW, + CW)
+        const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+        const uint32_t ob = tmem + lane_base + C::COL_O + ti * D;
         const float sl2 = p.scale_log2;
+        const int tl = row / p.GP, gl = row - tl * p.GP;   // the row's token and head in the tile
         if constexpr (REP > 1) {  // P is zero outside the copy's own keys
             uint32_t zero[32];
 #pragma unroll
@@ -488,16 +559,18 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         bool ok = true;
         int gj = 0, t = 0;
-        while (walk.next(p, ROWS, it)) {
-            const int r = it.rt * ROWS + row;
-            const int tok = r / p.G;
-            const bool live = tok < it.fresh;              // a new token's row
+        while (walk.next(p, it)) {
+            const int tok = it.tok0 + ti * p.TPT + tl;
+            const int head = it.g0 + gl;                   // among the key/value head's
+            const bool mine = tl < p.TPT && tok < p.T && head < p.G;  // a row of the call
+            const bool live = mine && tok < it.fresh;      // a new token's row
             const int nt = max(it.j1 - it.j0, 0);
             float m = -INFINITY;   // running maximum, base 2
             float l = 0.f;         // running sum
             float lr = 0.f;        // the same sum of the rounded weights
             for (int i = 0; ok && i < nt; ++i) {
                 const int g = gj + i;
+                const int b = bi(g, ti);
                 const int k0 = (it.j0 + i) * 128 + kw * CW;  // first key of this thread
                 // visibility of keys from the first new one on (held keys are all visible)
                 const bool need_mask = k0 + CW > it.past;
@@ -513,16 +586,19 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                                 bits = n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
                             } else {
                                 bits = x0 >= 0 ? 0u : (x0 <= -32 ? 0xffffffffu : (1u << -x0) - 1u);
-                                const uint8_t *mr = p.tree + it.b * p.tree_sb + (long long)tok * p.T;
-                                const int lo = max(0, -x0), hi = min(32, it.fresh - x0);
-                                for (int c = lo; c < hi; ++c)
-                                    bits |= (__ldg(mr + x0 + c) != 0 ? 1u : 0u) << c;
+                                const uint8_t *mr = p.tree + it.b * p.tree_sb + (long long)tok * p.T + x0;
+                                const int lo = max(0, -x0), n = min(32, it.fresh - x0);
+                                if (lo < n) {
+#pragma unroll
+                                    for (int c = 0; c < 32; ++c)
+                                        if (c >= lo && c < n) bits |= (__ldg(mr + c) != 0 ? 1u : 0u) << c;
+                                }
                             }
                         }
                         vis[w] = bits;
                     }
                 }
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[g & 1], (g / 2) & 1))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[b], ph(g)))) {
                     ok = false;
                     break;
                 }
@@ -530,13 +606,15 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 float s[CW];
                 {
                     uint32_t rr[CW];
-                    tmem_ldn<CW>(tmem + lane_base + C::COL_S + (g & 1) * 128 + kw * CW, rr);
+                    tmem_ldn<CW>(tmem + lane_base + C::COL_S + b * 128 + kw * CW, rr);
 #pragma unroll
                     for (int c = 0; c < CW; ++c) s[c] = __uint_as_float(rr[c]);
                 }
                 const uint32_t bad = bars->bad[g & 15];
-                tc_fence_before();
-                mbar_arrive(&bars->s_empty[g & 1]);
+                if (C::P_OWN) {
+                    tc_fence_before();
+                    mbar_arrive(&bars->s_empty[b]);
+                }
                 if (need_mask) {
 #pragma unroll
                     for (int c = 0; c < CW; ++c)
@@ -565,31 +643,15 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     m = mx;
                 }
                 const float m_use = (m == -INFINITY) ? 0.f : m;
-                float s0 = 0.f, s1 = 0.f, r0 = 0.f, r1 = 0.f;
-                uint32_t pk[CW / 2];
-#pragma unroll
-                for (int c = 0; c < CW; c += 2) {
-                    const float p0 = ex2(fmaf(s[c], sl2, -m_use));
-                    const float p1 = ex2(fmaf(s[c + 1], sl2, -m_use));
-                    s0 += p0;
-                    s1 += p1;
-                    pk[c >> 1] = pack2<BF16>(p0, p1);
-                    const float2 q = unpack2<BF16>(pk[c >> 1]);
-                    r0 += q.x;
-                    r1 += q.y;
-                }
-                l = l * alpha + (s0 + s1);
-                lr = lr * alpha + (r0 + r1);
-                // P's buffer is free once P_{g-2} V_{g-2} is done; O may be rescaled once
-                // P_{g-1} V_{g-1} is.
-                if (g >= 2 &&
-                    !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[g & 1], (g / 2 - 1) & 1))) {
+                // P's buffer is free once the last P V that read it is done (where P overwrites
+                // S it is); O may be rescaled once the previous tile's P V is.
+                if (g >= BUFS &&
+                    !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[b], ph(g - BUFS)))) {
                     ok = false;
                     break;
                 }
                 if (i > 0 && any_grow) {
-                    if (!__all_sync(0xffffffffu,
-                                    mbar_wait(&bars->pv_done[(g - 1) & 1], ((g - 1) / 2) & 1))) {
+                    if (RT == 1 && !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[bi(g - 1, ti)], ph(g - 1)))) {
                         ok = false;
                         break;
                     }
@@ -604,31 +666,35 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     }
                 }
                 tc_fence_after();
-                {
-                    const uint32_t pb = tmem + lane_base + C::COL_P + (g & 1) * 64 + kw * (CW / 2);
-                    if constexpr (CW == 32) {
-                        uint32_t rr[16];
+                float2 ls = make_float2(0.f, 0.f), rs = make_float2(0.f, 0.f);
+                const float2 sc = make_float2(sl2, sl2), nm = make_float2(-m_use, -m_use);
+                const uint32_t pb = tmem + lane_base + C::COL_P + b * C::P_STEP + kw * (CW / 2);
+                constexpr int STEP = CW < 64 ? CW : 64;    // weights of one TMEM store
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) rr[e] = pk[e];
-                        tmem_st16(pb, rr);
-                    } else {
+                for (int h = 0; h < CW / STEP; ++h) {
+                    uint32_t pk[STEP / 2];
 #pragma unroll
-                        for (int h = 0; h < CW / 64; ++h) {
-                            uint32_t rr[32];
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) rr[e] = pk[h * 32 + e];
-                            tmem_st32(pb + h * 32, rr);
-                        }
+                    for (int c = 0; c < STEP; c += 2) {
+                        const float2 x = fma2(make_float2(s[h * STEP + c], s[h * STEP + c + 1]), sc, nm);
+                        const float2 w = make_float2(ex2(x.x), ex2(x.y));
+                        ls = add2(ls, w);
+                        pk[c >> 1] = pack2<BF16>(w.x, w.y);
+                        rs = add2(rs, unpack2<BF16>(pk[c >> 1]));
                     }
+                    if constexpr (STEP == 32) tmem_st16(pb, pk);
+                    else tmem_st32(pb + h * 32, pk);
                 }
+                l = l * alpha + (ls.x + ls.y);
+                lr = lr * alpha + (rs.x + rs.y);
                 tc_fence_before();
-                mbar_arrive(&bars->p_full[g & 1]);
+                if (!C::P_OWN) mbar_arrive(&bars->s_empty[b]);
+                mbar_arrive(&bars->p_full[b]);
             }
 
             // ------------------------------ epilogue of the piece ------------------------
             if (ok && nt > 0) {
                 const int g = gj + nt - 1;
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[g & 1], (g / 2) & 1));
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[bi(g, ti)], ph(g)));
                 tc_fence_after();
             }
             // (the merge of the copies has barriers of all four warps: they leave together)
@@ -662,21 +728,15 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             const bool none = l == 0.f;                    // (a NaN sum is carried to O and LSE)
             const float inv = none ? 0.f : f / lr;
             const float lse2 = none ? -INFINITY : m + lg2(l);
-            const bool mine = r < p.G * p.T;               // a row of the call
-            const int h = it.hk * p.G + (r - tok * p.G);
             const long long slot = 2 * (long long)blockIdx.x + (it.index != 0 ? 1 : 0);
-            uint16_t *orow = const_cast<uint16_t *>(p.o.p) + it.b * p.o.sb + h * p.o.sh + tok * p.o.st;
-            float *prow = p.part_o + (slot * ROWS + row) * D;
-            float *merge = reinterpret_cast<float *>(smem + C::OFF_MERGE);
-            // Values that warp 6 cleared reach the rows that do see them (rare: only where a
-            // new key's V is not finite, and slow).
+            // Values that the repair cleared reach the rows that do see them (rare: only where
+            // a new key's V is not finite, and slow).
             const bool poison = nt > 0 && it.hides(p) && it.j1 * 128 > it.past && bars->poison[t & 3] != 0;
-            auto add_not_finite = [&](float *v, int n, int col) {
-                if (!live) return;
+            auto add_not_finite = [&](float *v, int n, int col, int tk) {
                 for (int j = max(it.past, it.j0 * 128); j < min(it.total, it.j1 * 128); ++j) {
                     const int x = j - it.past;
-                    const bool seen = p.tree ? p.tree[it.b * p.tree_sb + (long long)tok * p.T + x] != 0
-                                             : x <= tok;
+                    const bool seen = p.tree ? p.tree[it.b * p.tree_sb + (long long)tk * p.T + x] != 0
+                                             : x <= tk;
                     const int id = p.pt.table[(long long)it.b * p.pt.max_blocks + (j >> p.pt.page_shift)];
                     if (!seen || id < 0 || id >= p.pt.num_pages) continue;
                     const uint16_t *src = p.vc.p + id * p.vc.sb + it.hk * p.vc.sh +
@@ -687,126 +747,150 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     }
                 }
             };
+            auto out_row = [&](int h, int tk) {
+                return const_cast<uint16_t *>(p.o.p) + it.b * p.o.sb + (it.hk * p.G + h) * p.o.sh + tk * p.o.st;
+            };
+            const long long prow0 = slot * (RT * ROWS) + ti * ROWS;  // first row of the partial
+            if constexpr (REP == 1) {
 #pragma unroll
-            for (int c32 = 0; c32 < D / 32; ++c32) {
-                uint32_t rr[32];
-                if (nt > 0) {
-                    tmem_ld32(ob + c32 * 32, rr);
+                for (int c32 = 0; c32 < D / 32; ++c32) {
+                    float v[32];
+                    if (nt > 0) {
+                        uint32_t rr[32];
+                        tmem_ld32(ob + c32 * 32, rr);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        rr[e] = none ? 0u : __float_as_uint(__uint_as_float(rr[e]) * inv);
-                } else {
+                        for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : __uint_as_float(rr[e]) * inv;
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) rr[e] = 0u;
-                }
-                if (c32 == D / 32 - 1 && nt > 0) {
-                    tc_fence_before();
-                    mbar_arrive(&bars->o_empty);
-                }
-                if constexpr (REP == 1) {
-                    if (!mine) continue;
-                    if (poison) {
-                        float v[32];
-                        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(rr[e]);
-                        add_not_finite(v, 32, c32 * 32);
-                        for (int e = 0; e < 32; ++e) rr[e] = __float_as_uint(v[e]);
+                        for (int e = 0; e < 32; ++e) v[e] = 0.f;
                     }
+                    if (c32 == D / 32 - 1 && nt > 0) {
+                        tc_fence_before();
+                        mbar_arrive(&bars->o_empty);
+                    }
+                    if (!mine) continue;
+                    if (poison && live) add_not_finite(v, 32, c32 * 32, tok);
                     if (it.whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(orow) + c32 * 4;
+                        uint4 *dst = reinterpret_cast<uint4 *>(out_row(head, tok)) + c32 * 4;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            dst[e] = make_uint4(
-                                pack2<BF16>(__uint_as_float(rr[8 * e]), __uint_as_float(rr[8 * e + 1])),
-                                pack2<BF16>(__uint_as_float(rr[8 * e + 2]), __uint_as_float(rr[8 * e + 3])),
-                                pack2<BF16>(__uint_as_float(rr[8 * e + 4]), __uint_as_float(rr[8 * e + 5])),
-                                pack2<BF16>(__uint_as_float(rr[8 * e + 6]), __uint_as_float(rr[8 * e + 7])));
+                            dst[e] = make_uint4(pack2<BF16>(v[8 * e], v[8 * e + 1]),
+                                                pack2<BF16>(v[8 * e + 2], v[8 * e + 3]),
+                                                pack2<BF16>(v[8 * e + 4], v[8 * e + 5]),
+                                                pack2<BF16>(v[8 * e + 6], v[8 * e + 7]));
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(prow) + c32 * 8;
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + (prow0 + row) * D) + c32 * 8;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(__uint_as_float(rr[4 * e]), __uint_as_float(rr[4 * e + 1]),
-                                                 __uint_as_float(rr[4 * e + 2]), __uint_as_float(rr[4 * e + 3]));
+                            dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     }
-                } else {
-                    // sum of the copies: each warp lays its 32 x 32 block out (padded rows),
-                    // copy kw then sums columns [kw * 32 / REP, + 32 / REP) of its row
-                    float *buf = merge;
-                    if (c32 > 0) named_bar_sync(1, 128);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) buf[(warp * 32 + lane) * 33 + e] = __uint_as_float(rr[e]);
-                    named_bar_sync(1, 128);
-                    constexpr int N = 32 / REP;
-                    float v[N];
-#pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        v[e] = 0.f;
-#pragma unroll
-                        for (int k = 0; k < REP; ++k) v[e] += buf[(k * ROWS + row) * 33 + kw * N + e];
-                    }
-                    if (poison) add_not_finite(v, N, c32 * 32 + kw * N);
-                    if (mine) {
-                        if (it.whole) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(orow + c32 * 32 + kw * N);
-#pragma unroll
-                            for (int e = 0; e < N / 8; ++e)
-                                dst[e] = make_uint4(pack2<BF16>(v[8 * e], v[8 * e + 1]),
-                                                    pack2<BF16>(v[8 * e + 2], v[8 * e + 3]),
-                                                    pack2<BF16>(v[8 * e + 4], v[8 * e + 5]),
-                                                    pack2<BF16>(v[8 * e + 6], v[8 * e + 7]));
-                        } else {
-                            float4 *dst = reinterpret_cast<float4 *>(prow + c32 * 32 + kw * N);
-#pragma unroll
-                            for (int e = 0; e < N / 4; ++e)
-                                dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                }
+            } else {
+                // Sum of the copies through shared memory, all columns at once where the used
+                // rows are few, else 32 at a time; the threads then take the sums in rows of
+                // four columns.
+                float *buf = reinterpret_cast<float *>(smem + C::OFF_MERGE);
+                const int used = min(p.TPT, p.T) * p.GP;
+                const bool once = REP * used * (D + 4) * 4 <= C::MERGE;
+                const int cols = once ? D : 32, pitch = cols + 4;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += cols) {
+                    if (c0 > 0) named_bar_sync(1, 128);
+                    for (int c = 0; c < cols; c += 32) {
+                        uint32_t rr[32];
+                        if (nt > 0) {
+                            tmem_ld32(ob + c0 + c, rr);
+                            if (c0 + c == D - 32) {
+                                tc_fence_before();
+                                mbar_arrive(&bars->o_empty);
+                            }
                         }
+                        if (row < used) {
+                            float4 *dst = reinterpret_cast<float4 *>(buf + (kw * used + row) * pitch + c);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                dst[e] = (nt > 0 && !none)
+                                             ? make_float4(__uint_as_float(rr[4 * e]) * inv,
+                                                           __uint_as_float(rr[4 * e + 1]) * inv,
+                                                           __uint_as_float(rr[4 * e + 2]) * inv,
+                                                           __uint_as_float(rr[4 * e + 3]) * inv)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                    }
+                    named_bar_sync(1, 128);
+                    const int q = cols / 4;  // 8, 16 or 32
+                    for (int x = threadIdx.x; x < used * q; x += 128) {
+                        const int r = x / q, c = (x - r * q) * 4;
+                        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int k = 0; k < REP; ++k) {
+                            const float4 y = *reinterpret_cast<const float4 *>(buf + (k * used + r) * pitch + c);
+                            v[0] += y.x;
+                            v[1] += y.y;
+                            v[2] += y.z;
+                            v[3] += y.w;
+                        }
+                        const int rl = r / p.GP, tk = it.tok0 + rl, h = it.g0 + (r - rl * p.GP);
+                        if (tk >= p.T || h >= p.G) continue;
+                        if (poison && tk < it.fresh) add_not_finite(v, 4, c0 + c, tk);
+                        if (it.whole)
+                            *reinterpret_cast<uint2 *>(out_row(h, tk) + c0 + c) =
+                                make_uint2(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]));
+                        else
+                            *reinterpret_cast<float4 *>(p.part_o + (prow0 + r) * D + c0 + c) =
+                                make_float4(v[0], v[1], v[2], v[3]);
                     }
                 }
             }
             if (mine && kw == 0) {
                 if (it.whole)
-                    p.lse[((long long)it.b * p.Hk * p.G + h) * p.T + tok] =
+                    p.lse[((long long)it.b * p.Hk * p.G + it.hk * p.G + head) * p.T + tok] =
                         lse2 * 0.69314718055994531f;
                 else
-                    p.part_lse[slot * ROWS + row] = lse2;
+                    p.part_lse[prow0 + row] = lse2;
             }
-            if constexpr (REP > 1) named_bar_sync(1, 128);  // stat and the buffers are free again
+            if constexpr (REP > 1) named_bar_sync(1, 128);  // stat and the buffer are free again
             gj += nt;
             if (nt > 0) ++t;
         }
+    } else {
+        if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     }
 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 6) tmem_dealloc(tmem, 512);
+    if (warp == W_FIX) tmem_dealloc(tmem, 512);
 }
 
 // Merges the pieces of the items that were cut: with the pieces' log-sum-exps L_s (base 2),
 //   LSE = M + log2 sum_s 2^(L_s - M), O = sum_s 2^(L_s - LSE) O_s.
-// One warp per row; grid = (items, groups of 4 rows).
-template <int D, bool BF16>
+// One warp per row; grid = (items, groups of 4 rows).  `rows`: of a row tile.
+template <int D, bool BF16, int RT>
 __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_constant__ PagedParams p,
                                                              const int rows) {
-    pdl_wait();
-    pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int item = blockIdx.x;
     const int rt = item % p.row_tiles, hk = (item / p.row_tiles) % p.Hk, b = item / p.row_tiles / p.Hk;
-    const int row = blockIdx.y * 4 + warp;
-    const int r = rt * rows + row;
-    if (row >= rows || r >= p.T * p.G) return;
-    const PagedSeq s = paged_seq(p, rows, b);
+    const int row = blockIdx.y * 4 + warp;             // of the item
+    const int tile = row / rows, r = row - tile * rows;
+    const int tl = r / p.GP, tt = rt / p.GT;
+    const int tok = (tt * RT + tile) * p.TPT + tl, head = (rt - tt * p.GT) * p.GP + (r - tl * p.GP);
+    pdl_wait();
+    pdl_launch_dependents();
+    if (row >= RT * rows || tl >= p.TPT || tok >= p.T || head >= p.G) return;
+    const PagedSeq s = paged_seq<RT>(p, b);
     if (rt >= s.valid) return;
-    const long long W = paged_units(p, rows, lane, p.B), base = paged_units(p, rows, lane, b);
+    const long long W = paged_units<RT>(p, lane, p.B), base = paged_units<RT>(p, lane, b);
     const long long G = min((long long)p.ctas, W);
     const long long u0 = base + (long long)hk * s.per_head + (long long)rt * s.tiles, u1 = u0 + s.tiles;
     const int c0 = (int)(((u0 + 1) * G - 1) / W), c1 = (int)((u1 * G - 1) / W);
     if (c0 == c1) return;
     // the first piece lies in CTA c0's second slot if that share began before the item
     const int first = (c0 * W / G < u0) ? 1 : 0;
-    auto slot = [&](int c) -> long long { return 2LL * c + (c == c0 ? first : 0); };
+    auto at = [&](int c) -> long long { return (2LL * c + (c == c0 ? first : 0)) * (RT * rows) + row; };
     float M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_lse[slot(c) * rows + row]);
+    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_lse[at(c)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     constexpr int E = D / 32;  // columns of a lane
@@ -815,9 +899,9 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
     for (int c = c0; c <= c1; ++c) {
-        const float ls = p.part_lse[slot(c) * rows + row];
+        const float ls = p.part_lse[at(c)];
         const float w = ls == -INFINITY ? 0.f : ex2(ls - M);
-        const float *src = p.part_o + (slot(c) * rows + row) * D + lane * E;
+        const float *src = p.part_o + at(c) * D + lane * E;
         float v[E];
         if constexpr (E == 4) {
             const float4 x = *reinterpret_cast<const float4 *>(src);
@@ -831,7 +915,7 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
         for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e]);
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int tok = r / p.G, h = hk * p.G + (r - tok * p.G);
+    const int h = hk * p.G + head;
     uint16_t *o = const_cast<uint16_t *>(p.o.p) + b * p.o.sb + h * p.o.sh + tok * p.o.st + lane * E;
     if constexpr (E == 4)
         *reinterpret_cast<uint2 *>(o) = make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv),

@@ -64,8 +64,9 @@ def gather(cache, table, slots):
     return cache[table[slots // page].long(), :, slots % page].transpose(0, 1)
 
 
-def paged(q, k_cache, v_cache, table, cache_len, new_len, tree, scale):
-    """(o, lse, bound of o without rounding, bound of lse), all float64 numpy."""
+def paged(q, k_cache, v_cache, table, cache_len, new_len, tree, scale, heads=None):
+    """(o, lse, bound of o without rounding, bound of lse), all float64 numpy; of `heads`
+    only, where given."""
     B, H, T, d = q.shape
     Hk = k_cache.shape[1]
     dtype = q.dtype
@@ -85,7 +86,7 @@ def paged(q, k_cache, v_cache, table, cache_len, new_len, tree, scale):
             seen[:, past:] = m[:n, :n].numpy() != 0
         K = gather(k_cache, table[b], slots).double().numpy()
         V = gather(v_cache, table[b], slots).double().numpy()
-        for h in range(H):
+        for h in (range(H) if heads is None else heads):
             k, v = K[h // (H // Hk)], V[h // (H // Hk)]
             qq = q[b, h, :n].double().numpy()
             with np.errstate(all="ignore"):

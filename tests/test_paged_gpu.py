@@ -98,6 +98,32 @@ def test_matches_the_definition(case):
     against_reference(problem(B, Hk, G, T, d, page, lens, dtype, new=new, tree=tree, seed=len(lens) + T))
 
 
+LONG = [
+    # Every CTA's share wraps its ring of tiles several times and crosses items.
+    (6, 8, 2, 16, 64, 16, [6000, 11, 4097, 300, 0, 5555], FP, [16, 3, 16, 1, 9, 2], True),
+    (5, 8, 4, 12, 128, 32, [5000, 3000, 129, 7000, 900], BF, None, True),
+    (4, 8, 8, 13, 64, 64, [4000, 6100, 77, 2049], FP, None, False),
+    (4, 8, 8, 20, 128, 16, [3500, 6000, 1, 4444], BF, [20, 17, 20, 4], True),
+    (3, 8, 4, 70, 64, 128, [7000, 2500, 4100], BF, None, False),
+    (600, 4, 3, 1, 64, 16, [(97 * i) % 520 for i in range(600)], FP, None, False),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "-".join(str(x) for x in c[:6]))
+def test_long_shares(case):
+    B, Hk, G, T, d, page, lens, dtype, new, tree = case
+    c = problem(B, Hk, G, T, d, page, lens, dtype, new=new, tree=tree, seed=B)
+    o, lse = run(c)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK
+    heads = [0, Hk * G // 2 + 1, Hk * G - 1]
+    wo, wl, ob, lb = R.paged(c["q"], c["kc"], c["vc"], c["table"], c["cache_len"], c["new_len"],
+                             c["tree"], d ** -0.5, heads)
+    R.check("o", o[:, heads], wo[:, heads], (ob + R.rounding(wo, dtype))[:, heads])
+    R.check("lse", lse[:, heads], wl[:, heads], lb[:, heads])
+    assert torch.isfinite(o.float()).all()
+
+
 @pytest.mark.parametrize("T", [1, 3, 40])
 def test_rows_that_see_nothing(T):
     c = problem(3, 1, 3, T, 64, 16, [0, 5, 200], FP, tree=True, seed=4)
