@@ -1314,9 +1314,8 @@ int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *
     const int G = H / Hk;
     const PagedShape sh = paged_shape(G, T);
     const long long cap_tiles = ((long long)max_blocks * page_size + 127) / 128;
-    // units of one sequence and items of the call are counted in 32 bits
-    if ((double)sh.row_tiles * Hk * cap_tiles >= (double)(1LL << 31) ||
-        (double)sh.row_tiles * Hk * B >= (double)(1LL << 31))
+    // units of work are counted in 32 bits
+    if ((double)sh.row_tiles * Hk * B * (cap_tiles + fa::kItemCost) >= (double)(1LL << 31))
         return FA_ERR_UNSUPPORTED;
     int dev = 0;
     rc = check_device(&dev);
@@ -1335,6 +1334,7 @@ int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *
     p.G = G;
     p.T = T;
     p.GP = sh.GP;
+    p.gp_magic = (65536u + sh.GP - 1) / sh.GP;
     p.GT = sh.GT;
     p.TPT = sh.TPT;
     p.row_tiles = (int)sh.row_tiles;

@@ -19,7 +19,9 @@
 // launched early by PDL, merges them in a fixed order.
 //
 // CTA: softmax warps (one row per thread, 4 per row tile), then one producer warp (page table
-// and TMA of K and V), one MMA issuer, and one that loads Q and repairs V tiles (see repair).
+// and TMA of K and V), one MMA issuer, one that loads Q and repairs V tiles (see repair), and
+// one that works out the CTA's pieces of work ahead of the others and hands them over in
+// shared memory (its lookups of lengths, about 1 us an item, are off everybody's path).
 //
 // Few rows (REP = 4: a tile of 32 rows, REP = 2: 64): the rows are repeated in the tile's
 // REP lane quarters / halves, and each copy takes 1 / REP of the keys of every tile as a
@@ -46,6 +48,7 @@ struct PagedParams {
     float *part_o;       // [2 * gridDim.x][rows of an item][D]
     float *part_lse;     // [2 * gridDim.x][rows of an item], base 2
     int B, Hk, G, T;
+    unsigned gp_magic;   // r / GP = r * gp_magic >> 16 for r < 128
     int GP, GT;          // heads of a row tile; row tiles that a token's G heads take (1 up to
                          // 128 heads to a key/value head)
     int TPT;             // tokens of a row tile: (rows of a tile) / GP
@@ -70,12 +73,12 @@ struct PagedCfg {
     static constexpr int OFF_RING = OFF_Q + RT * QTILE;
     static constexpr int OFF_MERGE = OFF_RING + NS * TILE;
     static constexpr int OFF_BAR = OFF_MERGE + MERGE;
-    static constexpr int USED = OFF_BAR + 2560;
+    static constexpr int USED = OFF_BAR + 2816;
     static constexpr int SMEM = USED + 1024;
     static constexpr int SOFT = 4 * RT;         // softmax warps
-    // (two row tiles: whole warpgroups, so that registers can move from the other four warps
-    // to the softmax: 384 x 168 = 64512 at launch = 256 x 216 + 128 x 72)
-    static constexpr int THREADS = RT == 1 ? 224 : 384;
+    // (two row tiles: registers move from the other four warps to the softmax:
+    // 384 x 168 = 64512 at launch = 256 x 216 + 128 x 72)
+    static constexpr int THREADS = 32 * (SOFT + 4);
     // TMEM: two score buffers (RT = 1: alternating tiles; RT = 2: one per row tile).  P has
     // columns of its own except at d = 128 with two row tiles, where it overwrites S.
     static constexpr bool P_OWN = !(D == 128 && RT == 2);
@@ -97,9 +100,9 @@ struct PagedBars {
     // index: RT = 1 the tile's parity, RT = 2 the row tile
     uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
     uint64_t full[12], empty[12], fixed[12];  // per ring slot; fixed: V repaired
+    uint64_t seg_full[4], seg_empty[4];
     uint32_t tmem_base;
-    int b0;                 // this CTA's share: first sequence, its first unit, the share
-    long long base0, u0, u1;
+    int4 seg[4][3];         // ring of pieces (PagedSeg)
     uint32_t bad[16];       // per tile: sub-pages whose page number is outside the cache
     // Item t & 3 hides keys whose V is not finite.  (Four: the repairing warp reaches item
     // t + 4 only after the softmax of item t + 1 began.)
@@ -107,8 +110,10 @@ struct PagedBars {
     float stat[3][128];     // REP merge: m, l, l of the rounded weights
 };
 
-// Work units of a sequence: `tiles` per (head, item with new tokens), one for an item without
-// (its rows are written as empty).
+// Work units of a sequence: for each of its items with a new token the key tiles and kItemCost
+// for what an item costs by itself (its first scores, its epilogue: 1 to 2 us against 0.8 to
+// 1.5 us a tile), one for an item without (its rows are written as empty).
+constexpr int kItemCost = 1;
 struct PagedSeq {
     int past, fresh, tiles, valid;  // valid: items that hold a new token
     int per_head;
@@ -119,22 +124,38 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams &p, int b) {
     page_lengths(p.pt, p.T, b, s.past, s.fresh);
     s.tiles = (s.past + s.fresh + 127) >> 7;
     s.valid = (s.fresh + p.TPT * RT - 1) / (p.TPT * RT) * p.GT;
-    s.per_head = s.valid * s.tiles + (p.row_tiles - s.valid);
+    s.per_head = s.valid * (s.tiles + kItemCost) + (p.row_tiles - s.valid);
     return s;
 }
 
-// All units, and the sequence in which unit u lies with its first unit (one whole warp).
-__device__ __forceinline__ long long warp_sum(long long v) {
+__device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-template <int RT>
-__device__ __forceinline__ long long paged_units(const PagedParams &p, int lane, int upto) {
-    long long n = 0;
-    for (int b = lane; b < upto; b += 32) n += (long long)paged_seq<RT>(p, b).per_head * p.Hk;
-    return warp_sum(n);
+__device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive prefix sum
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    return v;
 }
+
+// The shares: W units over G CTAs, the first W % G of them with one unit more.
+struct PagedShares {
+    int q, extra;  // units of a share; shares with one more
+    __device__ __forceinline__ void init(int W, int ctas) {
+        const int G = max(min(ctas, W), 1);
+        q = W / G;
+        extra = W - q * G;
+    }
+    __device__ __forceinline__ int begin(int c) const { return c * q + min(c, extra); }
+    __device__ __forceinline__ int of(int u) const {  // the share of unit u
+        const int lead = extra * (q + 1);
+        return u < lead ? u / (q + 1) : extra + (u - lead) / q;
+    }
+};
 
 // One piece of work: key tiles [j0, j1) of one item.
 struct PagedSeg {
@@ -143,8 +164,8 @@ struct PagedSeg {
     int past, total;    // keys held, keys with the new ones
     int fresh;
     int j0, j1;
-    int index;          // 0: the share's first piece
-    bool whole;
+    int slot;           // of the workspace, if the item was cut
+    int whole;
     // Whether some row may see fewer new keys than another.
     __device__ __forceinline__ bool hides(const PagedParams &p) const {
         return fresh > 1 || p.tree != nullptr;
@@ -164,55 +185,120 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
     return __vcmpeq2(w & e, e);
 }
 
+// Hands this CTA's pieces over, in order (one whole warp; the lanes share the lookups).
 template <int RT>
-struct PagedWalk {
-    long long u, u1, base;
-    int b, index;
-    PagedSeq s;
-    __device__ __forceinline__ void init(const PagedParams &p, const PagedBars *bars) {
-        u = bars->u0;
-        u1 = bars->u1;
-        b = bars->b0;
-        base = bars->base0;
-        index = 0;
-        if (u < u1) s = paged_seq<RT>(p, b);
-    }
-    __device__ __forceinline__ bool next(const PagedParams &p, PagedSeg &g) {
-        if (u >= u1) return false;
-        while (u >= base + (long long)s.per_head * p.Hk) {
-            base += (long long)s.per_head * p.Hk;
-            s = paged_seq<RT>(p, ++b);
+__device__ __forceinline__ void paged_walk(const PagedParams &p, PagedBars *bars, int lane) {
+    // lengths of up to 32 sequences at a time, one per lane
+    int W = 0, k0 = 0, mine;
+    PagedSeq sq;
+    auto load = [&](int k) {
+        mine = 0;
+        if (k + lane < p.B) {
+            sq = paged_seq<RT>(p, k + lane);
+            mine = sq.per_head * p.Hk;
         }
-        const unsigned r0 = (unsigned)(u - base);
-        g.hk = (int)(r0 / (unsigned)s.per_head);
-        const int r = (int)(r0 - (unsigned)g.hk * (unsigned)s.per_head);
-        g.b = b;
-        g.past = s.past;
-        g.fresh = s.fresh;
-        g.total = s.past + s.fresh;
-        g.index = index++;
+    };
+    for (int k = 0; k < p.B; k += 32) {
+        load(k);
+        W += warp_sum(mine);
+    }
+    PagedShares sh;
+    sh.init(W, p.ctas);
+    const int c = blockIdx.x;
+    int u = min(sh.begin(c), W);
+    const int u1 = min(sh.begin(c + 1), W);
+    // the group of sequences with unit u
+    int base = 0, upto = 0;  // units before the group; inclusive sums within it
+    if (p.B > 32) load(0);
+    for (; u < u1; k0 += 32) {
+        upto = warp_scan(mine, lane);
+        const int all = __shfl_sync(0xffffffffu, upto, 31);
+        if (base + all > u) break;
+        base += all;
+        load(k0 + 32);
+    }
+    int n = 0;
+    auto put = [&](const PagedSeg &g) -> bool {
+        if (n >= 4 && !__all_sync(0xffffffffu, mbar_wait(&bars->seg_empty[n & 3], ((n >> 2) - 1) & 1)))
+            return false;
+        if (lane == 0) {
+            int4 *d = bars->seg[n & 3];
+            d[0] = make_int4(g.b, g.hk, g.tok0, g.g0);
+            d[1] = make_int4(g.past, g.total, g.fresh, g.j0);
+            d[2] = make_int4(g.j1, g.slot, g.whole, 0);
+            mbar_arrive(&bars->seg_full[n & 3]);
+        }
+        __syncwarp();
+        ++n;
+        return true;
+    };
+    PagedSeg g;
+    bool first = true;
+    while (u < u1) {
+        while (true) {  // the group with unit u
+            const int all = __shfl_sync(0xffffffffu, upto, 31);
+            if (base + all > u) break;
+            base += all;
+            k0 += 32;
+            load(k0);
+            upto = warp_scan(mine, lane);
+        }
+        const int f = __ffs(__ballot_sync(0xffffffffu, base + upto > u)) - 1;
+        const int r0 = u - base - __shfl_sync(0xffffffffu, upto - mine, f);
+        const int per_head = __shfl_sync(0xffffffffu, sq.per_head, f);
+        const int tiles = __shfl_sync(0xffffffffu, sq.tiles, f);
+        const int valid = __shfl_sync(0xffffffffu, sq.valid, f);
+        g.b = k0 + f;
+        g.past = __shfl_sync(0xffffffffu, sq.past, f);
+        g.fresh = __shfl_sync(0xffffffffu, sq.fresh, f);
+        g.total = g.past + g.fresh;
+        g.hk = (unsigned)r0 / (unsigned)per_head;
+        const int r = r0 - g.hk * per_head;
+        const int cost = tiles + kItemCost;
+        g.slot = 2 * c + (first ? 0 : 1);
+        first = false;
         int rt;
-        if (r < s.valid * s.tiles) {
-            rt = (int)((unsigned)r / (unsigned)s.tiles);
-            g.j0 = r - rt * s.tiles;
-            const long long left = u1 - u;
-            g.j1 = (int)min((long long)s.tiles, g.j0 + left);
-            u += g.j1 - g.j0;
-            g.whole = g.j0 == 0 && g.j1 == s.tiles;
+        if (r < valid * cost) {
+            rt = (unsigned)r / (unsigned)cost;
+            g.j0 = min(r - rt * cost, tiles);
+            const int end = min(cost, r - rt * cost + (u1 - u));
+            g.j1 = min(end, tiles);
+            u += end - (r - rt * cost);
+            if (g.j0 == g.j1) continue;  // nothing but the item's own cost
+            g.whole = g.j0 == 0 && g.j1 == tiles;
         } else {
-            rt = s.valid + (r - s.valid * s.tiles);
+            rt = valid + (r - valid * cost);
             g.j0 = g.j1 = 0;
-            g.whole = true;
+            g.whole = 1;
             u += 1;
         }
         const int tt = p.GT == 1 ? rt : rt / p.GT;
         g.tok0 = tt * RT * p.TPT;
         g.g0 = p.GT == 1 ? 0 : (rt - tt * p.GT) * p.GP;
         if (p.tree == nullptr)  // a chain's rows see no key behind their last token
-            g.j1 = min(g.j1, (s.past + min(s.fresh, g.tok0 + RT * p.TPT) + 127) >> 7);
-        return true;
+            g.j1 = min(g.j1, (g.past + min(g.fresh, g.tok0 + RT * p.TPT) + 127) >> 7);
+        if (!put(g)) return;
     }
-};
+    g.b = -1;
+    put(g);
+}
+
+// Takes piece n (all lanes that use it; lane 0 among them); false after the last one, or when
+// the wait gave up.
+__device__ __forceinline__ bool paged_take(PagedBars *bars, int n, int lane, bool warp_wide,
+                                           PagedSeg &g) {
+    bool ok = mbar_wait(&bars->seg_full[n & 3], (n >> 2) & 1);
+    if (warp_wide) ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    const int4 *d = bars->seg[n & 3];
+    const int4 x = d[0], y = d[1], z = d[2];
+    g.b = x.x, g.hk = x.y, g.tok0 = x.z, g.g0 = x.w;
+    g.past = y.x, g.total = y.y, g.fresh = y.z, g.j0 = y.w;
+    g.j1 = z.x, g.slot = z.y, g.whole = z.z;
+    if (warp_wide) __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->seg_empty[n & 3]);
+    return g.b >= 0;
+}
 
 __device__ __forceinline__ void tma_load_4d(void *smem_dst, const void *tmap, uint64_t *bar, int x,
                                             int y, int z, int w) {
@@ -258,13 +344,13 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     using C = PagedCfg<D, REP, RT>;
     constexpr int ROWS = C::ROWS;
     constexpr int CW = 128 / REP;     // keys of a tile that one thread handles
-    constexpr int W_TMA = C::SOFT, W_MMA = C::SOFT + 1, W_FIX = C::SOFT + 2;
+    constexpr int W_TMA = C::SOFT, W_MMA = C::SOFT + 1, W_FIX = C::SOFT + 2, W_WALK = C::SOFT + 3;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sQ = smem + C::OFF_Q;
     uint8_t *ring = smem + C::OFF_RING;
     PagedBars *bars = reinterpret_cast<PagedBars *>(smem + C::OFF_BAR);
-    static_assert(sizeof(PagedBars) <= 2560, "barrier area");
+    static_assert(sizeof(PagedBars) <= 2816, "barrier area");
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
@@ -293,57 +379,21 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             mbar_init(&bars->empty[i], 1);
             mbar_init(&bars->fixed[i], 1);
         }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bars->seg_full[i], 1);
+            mbar_init(&bars->seg_empty[i], C::SOFT + 3);
+        }
         fence_mbar_init();
     }
     if (warp == W_FIX) tmem_alloc(&bars->tmem_base, 512);
-    pdl_wait();
-    pdl_launch_dependents();
-    if (warp == W_TMA) {
-        if (blockIdx.x == 0)
-            for (int b = lane; b < p.B; b += 32) page_lengths_check(p.pt, p.T, b);
-        // this CTA's share of the units
-        const long long W = paged_units<RT>(p, lane, p.B);
-        const long long G = min((long long)p.ctas, W);
-        const long long c = blockIdx.x;
-        const long long u0 = c < G ? c * W / G : 0, u1 = c < G ? (c + 1) * W / G : 0;
-        // the sequence of u0: 32 sequences at a time
-        long long base = 0;
-        int b0 = 0;
-        if (u0 < u1) {
-            for (int k = 0; k < p.B; k += 32) {
-                const long long mine =
-                    k + lane < p.B ? (long long)paged_seq<RT>(p, k + lane).per_head * p.Hk : 0;
-                long long upto = mine;  // inclusive prefix sum
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += v;
-                }
-                const unsigned past = __ballot_sync(0xffffffffu, base + upto > u0);
-                if (past) {
-                    const int f = __ffs(past) - 1;
-                    b0 = k + f;
-                    base += __shfl_sync(0xffffffffu, upto - mine, f);
-                    break;
-                }
-                base += __shfl_sync(0xffffffffu, upto, 31);
-            }
-        }
-        if (lane == 0) {
-            bars->b0 = b0;
-            bars->base0 = base;
-            bars->u0 = u0;
-            bars->u1 = u1;
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_wait();
+    pdl_launch_dependents();
     const uint32_t tmem = bars->tmem_base;
-
-    PagedWalk<RT> walk;
-    walk.init(p, bars);
     PagedSeg it;
+    int np = 0;  // pieces taken
 
     if (warp == W_TMA) {
         // ------------------------------ K and V: whole warp -----------------------------
@@ -356,7 +406,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const int mine = lane % npt, half = lane / npt;
         int gj = 0;  // tiles so far
         bool ok = true;
-        while (ok && walk.next(p, it)) {
+        while (ok && paged_take(bars, np++, lane, true, it)) {
             const int *row = p.pt.table + (long long)it.b * p.pt.max_blocks;
             for (int j = it.j0; j < it.j1; ++j, ++gj) {
                 const int key = j * 128 + mine * box_rows;
@@ -434,7 +484,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             bool ok = true;
             int gj = 0, t = 0;
             uint32_t fixes = 0;  // parity of each slot's next repair
-            while (ok && walk.next(p, it)) {
+            while (ok && paged_take(bars, np++, lane, false, it)) {
                 const int nt = it.j1 - it.j0;
                 if (nt <= 0) continue;
                 if (!mbar_wait(&bars->q_full, t & 1)) break;
@@ -476,7 +526,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         bool ok = true;
         int gj = 0, t = 0, served = 0;
-        while (ok && walk.next(p, it)) {
+        while (ok && paged_take(bars, np++, lane, true, it)) {
             const int nt = it.j1 - it.j0;
             if (nt <= 0) continue;
             if (t > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (t - 1) & 1))) break;
@@ -549,7 +599,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
         const uint32_t ob = tmem + lane_base + C::COL_O + ti * D;
         const float sl2 = p.scale_log2;
-        const int tl = row / p.GP, gl = row - tl * p.GP;   // the row's token and head in the tile
+        const int tl = row * p.gp_magic >> 16, gl = row - tl * p.GP;  // the row's token and head
         if constexpr (REP > 1) {  // P is zero outside the copy's own keys
             uint32_t zero[32];
 #pragma unroll
@@ -559,7 +609,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         }
         bool ok = true;
         int gj = 0, t = 0;
-        while (walk.next(p, it)) {
+        while (paged_take(bars, np++, lane, true, it)) {
             const int tok = it.tok0 + ti * p.TPT + tl;
             const int head = it.g0 + gl;                   // among the key/value head's
             const bool mine = tl < p.TPT && tok < p.T && head < p.G;  // a row of the call
@@ -702,33 +752,9 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 if (nt > 0) ok = named_bar_and(1, 128, ok);
             if (!ok) break;
             if (!live) m = -INFINITY, l = lr = 0.f;  // rows behind the last new token are empty
-            // weights of the copies: O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) lr_k
-            float f = 1.f;
-            if constexpr (REP > 1) {
-                if (nt > 0) {
-                    bars->stat[0][threadIdx.x] = m;
-                    bars->stat[1][threadIdx.x] = l;
-                    bars->stat[2][threadIdx.x] = lr;
-                    named_bar_sync(1, 128);
-                    float M = -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < REP; ++k) M = fmaxf(M, bars->stat[0][k * ROWS + row]);
-                    f = (m == -INFINITY) ? 0.f : ex2(m - M);
-                    l = lr = 0.f;
-#pragma unroll
-                    for (int k = 0; k < REP; ++k) {
-                        const float mk = bars->stat[0][k * ROWS + row];
-                        const float fk = (mk == -INFINITY) ? 0.f : ex2(mk - M);
-                        l = fmaf(fk, bars->stat[1][k * ROWS + row], l);
-                        lr = fmaf(fk, bars->stat[2][k * ROWS + row], lr);
-                    }
-                    m = M;
-                }
-            }
             const bool none = l == 0.f;                    // (a NaN sum is carried to O and LSE)
-            const float inv = none ? 0.f : f / lr;
+            const float inv = none ? 0.f : 1.f / lr;
             const float lse2 = none ? -INFINITY : m + lg2(l);
-            const long long slot = 2 * (long long)blockIdx.x + (it.index != 0 ? 1 : 0);
             // Values that the repair cleared reach the rows that do see them (rare: only where
             // a new key's V is not finite, and slow).
             const bool poison = nt > 0 && it.hides(p) && it.j1 * 128 > it.past && bars->poison[t & 3] != 0;
@@ -750,7 +776,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             auto out_row = [&](int h, int tk) {
                 return const_cast<uint16_t *>(p.o.p) + it.b * p.o.sb + (it.hk * p.G + h) * p.o.sh + tk * p.o.st;
             };
-            const long long prow0 = slot * (RT * ROWS) + ti * ROWS;  // first row of the partial
+            const long long prow0 = (long long)it.slot * (RT * ROWS) + ti * ROWS;  // first row of the partial
             if constexpr (REP == 1) {
 #pragma unroll
                 for (int c32 = 0; c32 < D / 32; ++c32) {
@@ -785,76 +811,102 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                             dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     }
                 }
+                if (mine) {
+                    if (it.whole)
+                        p.lse[((long long)it.b * p.Hk * p.G + it.hk * p.G + head) * p.T + tok] =
+                            lse2 * 0.69314718055994531f;
+                    else
+                        p.part_lse[prow0 + row] = lse2;
+                }
             } else {
-                // Sum of the copies through shared memory, all columns at once where the used
-                // rows are few, else 32 at a time; the threads then take the sums in rows of
-                // four columns.
+                // The copies meet in shared memory (the vote above is also the barrier behind
+                // the last piece's reads): sums, maxima and unscaled O, all columns at once
+                // where the used rows are few, else 32 at a time.  With weights
+                // f_k = 2^(m_k - M), O = sum_k f_k O_k / sum_k f_k lr_k.
                 float *buf = reinterpret_cast<float *>(smem + C::OFF_MERGE);
                 const int used = min(p.TPT, p.T) * p.GP;
                 const bool once = REP * used * (D + 4) * 4 <= C::MERGE;
-                const int cols = once ? D : 32, pitch = cols + 4;
+                const int pitch = (once ? D : 32) + 4;
+                const int qs = once ? (D == 64 ? 4 : 5) : 3;   // log2 of 4-column groups
+                const int x = wq * 32 + lane;
+                const int c4 = (x & ((1 << qs) - 1)) * 4;      // this thread's columns
+                if (nt > 0) {
+                    bars->stat[0][x] = m;
+                    bars->stat[1][x] = l;
+                    bars->stat[2][x] = lr;
+                }
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += cols) {
-                    if (c0 > 0) named_bar_sync(1, 128);
-                    for (int c = 0; c < cols; c += 32) {
-                        uint32_t rr[32];
-                        if (nt > 0) {
+                for (int c0 = 0; c0 < D; c0 += pitch - 4) {
+                    if (nt > 0) {
+                        if (c0 > 0) named_bar_sync(1, 128);
+                        for (int c = 0; c < pitch - 4; c += 32) {
+                            uint32_t rr[32];
                             tmem_ld32(ob + c0 + c, rr);
                             if (c0 + c == D - 32) {
                                 tc_fence_before();
                                 mbar_arrive(&bars->o_empty);
                             }
-                        }
-                        if (row < used) {
-                            float4 *dst = reinterpret_cast<float4 *>(buf + (kw * used + row) * pitch + c);
+                            if (row < used) {
+                                uint4 *dst = reinterpret_cast<uint4 *>(buf + (kw * used + row) * pitch + c);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                dst[e] = (nt > 0 && !none)
-                                             ? make_float4(__uint_as_float(rr[4 * e]) * inv,
-                                                           __uint_as_float(rr[4 * e + 1]) * inv,
-                                                           __uint_as_float(rr[4 * e + 2]) * inv,
-                                                           __uint_as_float(rr[4 * e + 3]) * inv)
-                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                                for (int e = 0; e < 8; ++e)
+                                    dst[e] = make_uint4(rr[4 * e], rr[4 * e + 1], rr[4 * e + 2], rr[4 * e + 3]);
+                            }
                         }
+                        named_bar_sync(1, 128);
                     }
-                    named_bar_sync(1, 128);
-                    const int q = cols / 4;  // 8, 16 or 32
-                    for (int x = threadIdx.x; x < used * q; x += 128) {
-                        const int r = x / q, c = (x - r * q) * 4;
-                        float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int k = 0; k < REP; ++k) {
-                            const float4 y = *reinterpret_cast<const float4 *>(buf + (k * used + r) * pitch + c);
-                            v[0] += y.x;
-                            v[1] += y.y;
-                            v[2] += y.z;
-                            v[3] += y.w;
-                        }
-                        const int rl = r / p.GP, tk = it.tok0 + rl, h = it.g0 + (r - rl * p.GP);
+                    for (int r = x >> qs; r < used; r += 128 >> qs) {
+                        const int rl = r * p.gp_magic >> 16, tk = it.tok0 + rl, h = it.g0 + (r - rl * p.GP);
                         if (tk >= p.T || h >= p.G) continue;
-                        if (poison && tk < it.fresh) add_not_finite(v, 4, c0 + c, tk);
+                        float v[4] = {0.f, 0.f, 0.f, 0.f};
+                        float ls2 = -INFINITY;
+                        if (nt > 0 && tk < it.fresh) {
+                            float M = -INFINITY, L = 0.f, R = 0.f;
+#pragma unroll
+                            for (int k = 0; k < REP; ++k) M = fmaxf(M, bars->stat[0][k * ROWS + r]);
+#pragma unroll
+                            for (int k = 0; k < REP; ++k) {
+                                const float mk = bars->stat[0][k * ROWS + r];
+                                const float fk = (mk == -INFINITY) ? 0.f : ex2(mk - M);
+                                const float4 y = *reinterpret_cast<const float4 *>(buf + (k * used + r) * pitch + c4);
+                                L = fmaf(fk, bars->stat[1][k * ROWS + r], L);
+                                R = fmaf(fk, bars->stat[2][k * ROWS + r], R);
+                                v[0] = fmaf(fk, y.x, v[0]);
+                                v[1] = fmaf(fk, y.y, v[1]);
+                                v[2] = fmaf(fk, y.z, v[2]);
+                                v[3] = fmaf(fk, y.w, v[3]);
+                            }
+                            const float iv = L == 0.f ? 0.f : 1.f / R;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = L == 0.f ? 0.f : v[e] * iv;
+                            if (L != 0.f) ls2 = M + lg2(L);
+                            if (poison) add_not_finite(v, 4, c0 + c4, tk);
+                        }
                         if (it.whole)
-                            *reinterpret_cast<uint2 *>(out_row(h, tk) + c0 + c) =
+                            *reinterpret_cast<uint2 *>(out_row(h, tk) + c0 + c4) =
                                 make_uint2(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]));
                         else
-                            *reinterpret_cast<float4 *>(p.part_o + (prow0 + r) * D + c0 + c) =
+                            *reinterpret_cast<float4 *>(p.part_o + (prow0 + r) * D + c0 + c4) =
                                 make_float4(v[0], v[1], v[2], v[3]);
+                        if (c0 == 0 && c4 == 0) {
+                            if (it.whole)
+                                p.lse[((long long)it.b * p.Hk * p.G + it.hk * p.G + h) * p.T + tk] =
+                                    ls2 * 0.69314718055994531f;
+                            else
+                                p.part_lse[prow0 + r] = ls2;
+                        }
                     }
                 }
             }
-            if (mine && kw == 0) {
-                if (it.whole)
-                    p.lse[((long long)it.b * p.Hk * p.G + it.hk * p.G + head) * p.T + tok] =
-                        lse2 * 0.69314718055994531f;
-                else
-                    p.part_lse[prow0 + row] = lse2;
-            }
-            if constexpr (REP > 1) named_bar_sync(1, 128);  // stat and the buffer are free again
             gj += nt;
             if (nt > 0) ++t;
         }
     } else {
+        // ------------------------------ pieces of work ----------------------------------
         if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (blockIdx.x == 0)
+            for (int b = lane; b < p.B; b += 32) page_lengths_check(p.pt, p.T, b);
+        paged_walk<RT>(p, bars, lane);
     }
 
     tc_fence_before();
@@ -874,20 +926,28 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
     const int rt = item % p.row_tiles, hk = (item / p.row_tiles) % p.Hk, b = item / p.row_tiles / p.Hk;
     const int row = blockIdx.y * 4 + warp;             // of the item
     const int tile = row / rows, r = row - tile * rows;
-    const int tl = r / p.GP, tt = rt / p.GT;
+    const int tl = r * p.gp_magic >> 16, tt = rt / p.GT;
     const int tok = (tt * RT + tile) * p.TPT + tl, head = (rt - tt * p.GT) * p.GP + (r - tl * p.GP);
     pdl_wait();
     pdl_launch_dependents();
     if (row >= RT * rows || tl >= p.TPT || tok >= p.T || head >= p.G) return;
     const PagedSeq s = paged_seq<RT>(p, b);
     if (rt >= s.valid) return;
-    const long long W = paged_units<RT>(p, lane, p.B), base = paged_units<RT>(p, lane, b);
-    const long long G = min((long long)p.ctas, W);
-    const long long u0 = base + (long long)hk * s.per_head + (long long)rt * s.tiles, u1 = u0 + s.tiles;
-    const int c0 = (int)(((u0 + 1) * G - 1) / W), c1 = (int)((u1 * G - 1) / W);
+    int W = 0, base = 0;  // all units, those before the sequence
+    for (int k = lane; k < p.B; k += 32) {
+        const int n = paged_seq<RT>(p, k).per_head * p.Hk;
+        W += n;
+        base += k < b ? n : 0;
+    }
+    W = warp_sum(W);
+    base = warp_sum(base);
+    PagedShares sh;
+    sh.init(W, p.ctas);
+    const int u0 = base + hk * s.per_head + rt * (s.tiles + kItemCost);
+    const int c0 = sh.of(u0), c1 = sh.of(u0 + s.tiles - 1);
     if (c0 == c1) return;
     // the first piece lies in CTA c0's second slot if that share began before the item
-    const int first = (c0 * W / G < u0) ? 1 : 0;
+    const int first = sh.begin(c0) < u0 ? 1 : 0;
     auto at = [&](int c) -> long long { return (2LL * c + (c == c0 ? first : 0)) * (RT * rows) + row; };
     float M = -INFINITY;
     for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_lse[at(c)]);
