@@ -73,11 +73,9 @@ struct PagedCfg {
     static constexpr int OFF_RING = OFF_Q + RT * QTILE;
     static constexpr int OFF_MERGE = OFF_RING + NS * TILE;
     static constexpr int OFF_BAR = OFF_MERGE + MERGE;
-    static constexpr int USED = OFF_BAR + 2816;
+    static constexpr int USED = OFF_BAR + 2816 + 4096;
     static constexpr int SMEM = USED + 1024;
     static constexpr int SOFT = 4 * RT;         // softmax warps
-    // (two row tiles: registers move from the other four warps to the softmax:
-    // 384 x 168 = 64512 at launch = 256 x 216 + 128 x 72)
     static constexpr int THREADS = 32 * (SOFT + 4);
     // TMEM: two score buffers (RT = 1: alternating tiles; RT = 2: one per row tile).  P has
     // columns of its own except at d = 128 with two row tiles, where it overwrites S.
@@ -108,6 +106,7 @@ struct PagedBars {
     // t + 4 only after the softmax of item t + 1 began.)
     int poison[4];
     float stat[3][128];     // REP merge: m, l, l of the rounded weights
+    uint32_t vis[4][256];   // per softmax thread: keys of the tile that its row sees
 };
 
 // Work units of a sequence: for each of its items with a new token the key tiles and kItemCost
@@ -317,6 +316,20 @@ __device__ __forceinline__ void tmem_ldn(uint32_t a, uint32_t (&r)[C]) {
     else tmem_ld32(a, r);
 }
 
+// Registers -> TMEM, 32 lanes x 16 columns, complete after tmem_wait_st().
+__device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // Two fp32 operations at once (packed registers).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -350,7 +363,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint8_t *sQ = smem + C::OFF_Q;
     uint8_t *ring = smem + C::OFF_RING;
     PagedBars *bars = reinterpret_cast<PagedBars *>(smem + C::OFF_BAR);
-    static_assert(sizeof(PagedBars) <= 2816, "barrier area");
+    static_assert(sizeof(PagedBars) <= 2816 + 4096, "barrier area");
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
@@ -397,7 +410,6 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 
     if (warp == W_TMA) {
         // ------------------------------ K and V: whole warp -----------------------------
-        if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // A tile's pages: npt boxes (a page, or 128 rows of a larger one) per 64-element
         // column block; lane l loads box l % npt of block l / npt.
         const int page = 1 << p.pt.page_shift;
@@ -443,7 +455,6 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 (void)mbar_wait(&bars->full[n % C::NS], (n / C::NS) & 1);
     } else if (warp == W_MMA) {
         // ------------------------------ MMA issuer --------------------------------------
-        if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (lane == 0) {
             constexpr uint32_t kIdescS = idesc_f16(BF16, false, false, 128, 128);
             constexpr uint32_t kIdescO = idesc_f16(BF16, false, true, 128, D);
@@ -523,7 +534,6 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         }
     } else if (warp == W_FIX) {
         // ------------------------------ Q loads, V repairs ------------------------------
-        if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         bool ok = true;
         int gj = 0, t = 0, served = 0;
         while (ok && paged_take(bars, np++, lane, true, it)) {
@@ -590,7 +600,6 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         if (t > 0) (void)mbar_wait(&bars->q_full, (t - 1) & 1);
     } else if (warp < C::SOFT) {
         // ------------------------------ softmax warps -----------------------------------
-        if constexpr (RT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         constexpr int WPC = 4 / REP;                       // warps of one copy of the rows
         const int ti = RT == 1 ? 0 : warp >> 2;            // row tile
         const int wq = warp & 3;                           // lane quarter of TMEM
@@ -622,11 +631,11 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 const int g = gj + i;
                 const int b = bi(g, ti);
                 const int k0 = (it.j0 + i) * 128 + kw * CW;  // first key of this thread
-                // visibility of keys from the first new one on (held keys are all visible)
-                const bool need_mask = k0 + CW > it.past;
-                uint32_t vis[CW / 32];
-                if (need_mask) {
-#pragma unroll
+                const uint32_t sb = tmem + lane_base + C::COL_S + b * 128 + kw * CW;
+                // Keys from the first new one on: the row's visible ones (held keys all are).
+                bool masked = k0 + CW > it.past;
+                if (masked) {
+#pragma unroll 1
                     for (int w = 0; w < CW / 32; ++w) {
                         const int x0 = k0 + w * 32 - it.past;  // new key of bit 0
                         uint32_t bits = 0u;
@@ -645,7 +654,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                                 }
                             }
                         }
-                        vis[w] = bits;
+                        bars->vis[w][threadIdx.x] = bits;
                     }
                 }
                 if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[b], ph(g)))) {
@@ -653,38 +662,51 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     break;
                 }
                 tc_fence_after();
-                float s[CW];
-                {
-                    uint32_t rr[CW];
-                    tmem_ldn<CW>(tmem + lane_base + C::COL_S + b * 128 + kw * CW, rr);
-#pragma unroll
-                    for (int c = 0; c < CW; ++c) s[c] = __uint_as_float(rr[c]);
-                }
                 const uint32_t bad = bars->bad[g & 15];
-                if (C::P_OWN) {
-                    tc_fence_before();
-                    mbar_arrive(&bars->s_empty[b]);
-                }
-                if (need_mask) {
+                // First pass over the scores: the maximum.  (The passes read the scores from
+                // TMEM 32 or 64 at a time in loops: unrolled over a row's 128 the code took
+                // 4 us to come in from memory at a kernel's first tile, against 1.1 us a tile
+                // once there.)  Hidden scores become -inf in TMEM, so that one masking serves
+                // both passes.
+                float mxv[4];
 #pragma unroll
-                    for (int c = 0; c < CW; ++c)
-                        if (!((vis[c >> 5] >> (c & 31)) & 1u)) s[c] = -INFINITY;
-                }
-                if (bad) {  // keys of pages outside the cache are not visible
-                    const int sh = min(p.pt.page_shift, 7);
+                for (int e = 0; e < 4; ++e) mxv[e] = -INFINITY;
+                if (masked || bad != 0) {
+#pragma unroll 1
+                    for (int w = 0; w < CW / 32; ++w) {
+                        uint32_t bits = masked ? bars->vis[w][threadIdx.x] : 0xffffffffu;
+                        if (bad) {  // keys of pages outside the cache are not visible
+                            const int sh = min(p.pt.page_shift, 7), n = min(1 << sh, 32);
+                            for (int c = 0; c < 32; c += n)
+                                if ((bad >> ((kw * CW + w * 32 + c) >> sh)) & 1u)
+                                    bits &= ~((n == 32 ? 0xffffffffu : (1u << n) - 1u) << c);
+                        }
+                        uint32_t rr[32];
+                        tmem_ld32(sb + w * 32, rr);
 #pragma unroll
-                    for (int c = 0; c < CW; ++c)
-                        if ((bad >> ((kw * CW + c) >> sh)) & 1u) s[c] = -INFINITY;
-                }
-                float mxv[8];
+                        for (int c = 0; c < 32; ++c)
+                            if (!((bits >> c) & 1u)) rr[c] = 0xff800000u;
+                        tmem_st32(sb + w * 32, rr);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    mxv[e] = fmaxf(s[e], s[8 + e]);
+                        for (int c = 0; c < 32; c += 8)
 #pragma unroll
-                    for (int c = 16; c < CW; c += 16) mxv[e] = fmax3(mxv[e], s[c + e], s[c + 8 + e]);
+                            for (int e = 0; e < 4; ++e)
+                                mxv[e] = fmax3(mxv[e], __uint_as_float(rr[c + e]), __uint_as_float(rr[c + 4 + e]));
+                    }
+                } else {
+                    constexpr int N = CW < 64 ? CW : 64;
+#pragma unroll 1
+                    for (int w = 0; w < CW / N; ++w) {
+                        uint32_t rr[N];
+                        tmem_ldn<N>(sb + w * N, rr);
+#pragma unroll
+                        for (int c = 0; c < N; c += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                mxv[e] = fmax3(mxv[e], __uint_as_float(rr[c + e]), __uint_as_float(rr[c + 4 + e]));
+                    }
                 }
-                const float mx = fmax3(fmax3(mxv[0], mxv[1], mxv[2]), fmax3(mxv[3], mxv[4], mxv[5]),
-                                       fmaxf(mxv[6], mxv[7])) * sl2;
+                const float mx = fmaxf(fmax3(mxv[0], mxv[1], mxv[2]), mxv[3]) * sl2;
                 // Lazy rescale: m moves when the maximum grew by more than 2^8.
                 const bool any_grow = __any_sync(0xffffffffu, mx > m + 8.0f);
                 float alpha = 1.f;
@@ -706,7 +728,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         break;
                     }
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t rr[32];
                         tmem_ld32(ob + c * 32, rr);
@@ -716,28 +738,46 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     }
                 }
                 tc_fence_after();
+                // Second pass: the weights, their sums, P.  (P overwrites S behind the reads.)
                 float2 ls = make_float2(0.f, 0.f), rs = make_float2(0.f, 0.f);
                 const float2 sc = make_float2(sl2, sl2), nm = make_float2(-m_use, -m_use);
                 const uint32_t pb = tmem + lane_base + C::COL_P + b * C::P_STEP + kw * (CW / 2);
-                constexpr int STEP = CW < 64 ? CW : 64;    // weights of one TMEM store
+                auto weights = [&](const uint32_t (&rr)[32], uint32_t dst) {
+                    uint32_t pk[16];
 #pragma unroll
-                for (int h = 0; h < CW / STEP; ++h) {
-                    uint32_t pk[STEP / 2];
-#pragma unroll
-                    for (int c = 0; c < STEP; c += 2) {
-                        const float2 x = fma2(make_float2(s[h * STEP + c], s[h * STEP + c + 1]), sc, nm);
+                    for (int c = 0; c < 32; c += 2) {
+                        const float2 x = fma2(make_float2(__uint_as_float(rr[c]), __uint_as_float(rr[c + 1])), sc, nm);
                         const float2 w = make_float2(ex2(x.x), ex2(x.y));
                         ls = add2(ls, w);
                         pk[c >> 1] = pack2<BF16>(w.x, w.y);
                         rs = add2(rs, unpack2<BF16>(pk[c >> 1]));
                     }
-                    if constexpr (STEP == 32) tmem_st16(pb, pk);
-                    else tmem_st32(pb + h * 32, pk);
+                    tmem_st16_async(dst, pk);
+                };
+                {
+                    uint32_t ra[32], rb[32];
+                    tmem_ld32(sb, ra);
+                    if constexpr (CW == 32) {
+                        weights(ra, pb);
+                    } else {
+#pragma unroll 1
+                        for (int w = 0; w < CW / 32; w += 2) {  // the next 32 are on their way
+                            tmem_ld32_async(sb + (w + 1) * 32, rb);
+                            weights(ra, pb + w * 16);
+                            tmem_wait_ld(rb);
+                            // (behind the last: a load that nobody uses, so that the loop's
+                            // registers are not merged before the wait)
+                            tmem_ld32_async(sb + min(w + 2, CW / 32 - 1) * 32, ra);
+                            weights(rb, pb + (w + 1) * 16);
+                            tmem_wait_ld(ra);
+                        }
+                    }
+                    tmem_wait_st();
                 }
                 l = l * alpha + (ls.x + ls.y);
                 lr = lr * alpha + (rs.x + rs.y);
                 tc_fence_before();
-                if (!C::P_OWN) mbar_arrive(&bars->s_empty[b]);
+                mbar_arrive(&bars->s_empty[b]);
                 mbar_arrive(&bars->p_full[b]);
             }
 
@@ -752,9 +792,9 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 if (nt > 0) ok = named_bar_and(1, 128, ok);
             if (!ok) break;
             if (!live) m = -INFINITY, l = lr = 0.f;  // rows behind the last new token are empty
-            const bool none = l == 0.f;                    // (a NaN sum is carried to O and LSE)
+            bool none = l == 0.f;                    // (a NaN sum is carried to O and LSE)
             const float inv = none ? 0.f : 1.f / lr;
-            const float lse2 = none ? -INFINITY : m + lg2(l);
+            float lse2 = none ? -INFINITY : m + lg2(l);
             // Values that the repair cleared reach the rows that do see them (rare: only where
             // a new key's V is not finite, and slow).
             const bool poison = nt > 0 && it.hides(p) && it.j1 * 128 > it.past && bars->poison[t & 3] != 0;
@@ -778,7 +818,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             };
             const long long prow0 = (long long)it.slot * (RT * ROWS) + ti * ROWS;  // first row of the partial
             if constexpr (REP == 1) {
-#pragma unroll
+#pragma unroll 1
                 for (int c32 = 0; c32 < D / 32; ++c32) {
                     float v[32];
                     if (nt > 0) {
@@ -811,18 +851,11 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                             dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     }
                 }
-                if (mine) {
-                    if (it.whole)
-                        p.lse[((long long)it.b * p.Hk * p.G + it.hk * p.G + head) * p.T + tok] =
-                            lse2 * 0.69314718055994531f;
-                    else
-                        p.part_lse[prow0 + row] = lse2;
-                }
             } else {
                 // The copies meet in shared memory (the vote above is also the barrier behind
-                // the last piece's reads): sums, maxima and unscaled O, all columns at once
-                // where the used rows are few, else 32 at a time.  With weights
-                // f_k = 2^(m_k - M), O = sum_k f_k O_k / sum_k f_k lr_k.
+                // the last piece's reads): first their maxima and sums, then O scaled by
+                // f_k / R, f_k = 2^(m_k - M), R = sum_k f_k lr_k, all columns at once where the
+                // used rows are few, else 32 at a time.  O = sum_k (f_k / R) O_k.
                 float *buf = reinterpret_cast<float *>(smem + C::OFF_MERGE);
                 const int used = min(p.TPT, p.T) * p.GP;
                 const bool once = REP * used * (D + 4) * 4 <= C::MERGE;
@@ -830,15 +863,31 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 const int qs = once ? (D == 64 ? 4 : 5) : 3;   // log2 of 4-column groups
                 const int x = wq * 32 + lane;
                 const int c4 = (x & ((1 << qs) - 1)) * 4;      // this thread's columns
+                float scale = 0.f;
                 if (nt > 0) {
                     bars->stat[0][x] = m;
                     bars->stat[1][x] = l;
                     bars->stat[2][x] = lr;
+                    named_bar_sync(1, 128);
+                    float M = -INFINITY, L = 0.f, R = 0.f;
+#pragma unroll
+                    for (int k = 0; k < REP; ++k) M = fmaxf(M, bars->stat[0][k * ROWS + row]);
+#pragma unroll
+                    for (int k = 0; k < REP; ++k) {
+                        const float mk = bars->stat[0][k * ROWS + row];
+                        const float fk = (mk == -INFINITY) ? 0.f : ex2(mk - M);
+                        L = fmaf(fk, bars->stat[1][k * ROWS + row], L);
+                        R = fmaf(fk, bars->stat[2][k * ROWS + row], R);
+                    }
+                    none = L == 0.f;
+                    scale = ((m == -INFINITY) ? 0.f : ex2(m - M)) / R;
+                    lse2 = none ? -INFINITY : M + lg2(L);
                 }
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += pitch - 4) {
                     if (nt > 0) {
                         if (c0 > 0) named_bar_sync(1, 128);
+#pragma unroll 1
                         for (int c = 0; c < pitch - 4; c += 32) {
                             uint32_t rr[32];
                             tmem_ld32(ob + c0 + c, rr);
@@ -847,63 +896,55 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                                 mbar_arrive(&bars->o_empty);
                             }
                             if (row < used) {
-                                uint4 *dst = reinterpret_cast<uint4 *>(buf + (kw * used + row) * pitch + c);
+                                float4 *dst = reinterpret_cast<float4 *>(buf + (kw * used + row) * pitch + c);
 #pragma unroll
                                 for (int e = 0; e < 8; ++e)
-                                    dst[e] = make_uint4(rr[4 * e], rr[4 * e + 1], rr[4 * e + 2], rr[4 * e + 3]);
+                                    dst[e] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                  : make_float4(__uint_as_float(rr[4 * e]) * scale,
+                                                                __uint_as_float(rr[4 * e + 1]) * scale,
+                                                                __uint_as_float(rr[4 * e + 2]) * scale,
+                                                                __uint_as_float(rr[4 * e + 3]) * scale);
                             }
                         }
                         named_bar_sync(1, 128);
                     }
+#pragma unroll 2
                     for (int r = x >> qs; r < used; r += 128 >> qs) {
-                        const int rl = r * p.gp_magic >> 16, tk = it.tok0 + rl, h = it.g0 + (r - rl * p.GP);
-                        if (tk >= p.T || h >= p.G) continue;
                         float v[4] = {0.f, 0.f, 0.f, 0.f};
-                        float ls2 = -INFINITY;
-                        if (nt > 0 && tk < it.fresh) {
-                            float M = -INFINITY, L = 0.f, R = 0.f;
-#pragma unroll
-                            for (int k = 0; k < REP; ++k) M = fmaxf(M, bars->stat[0][k * ROWS + r]);
+                        if (nt > 0) {
 #pragma unroll
                             for (int k = 0; k < REP; ++k) {
-                                const float mk = bars->stat[0][k * ROWS + r];
-                                const float fk = (mk == -INFINITY) ? 0.f : ex2(mk - M);
                                 const float4 y = *reinterpret_cast<const float4 *>(buf + (k * used + r) * pitch + c4);
-                                L = fmaf(fk, bars->stat[1][k * ROWS + r], L);
-                                R = fmaf(fk, bars->stat[2][k * ROWS + r], R);
-                                v[0] = fmaf(fk, y.x, v[0]);
-                                v[1] = fmaf(fk, y.y, v[1]);
-                                v[2] = fmaf(fk, y.z, v[2]);
-                                v[3] = fmaf(fk, y.w, v[3]);
+                                v[0] += y.x;
+                                v[1] += y.y;
+                                v[2] += y.z;
+                                v[3] += y.w;
                             }
-                            const float iv = L == 0.f ? 0.f : 1.f / R;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) v[e] = L == 0.f ? 0.f : v[e] * iv;
-                            if (L != 0.f) ls2 = M + lg2(L);
-                            if (poison) add_not_finite(v, 4, c0 + c4, tk);
                         }
+                        const int rl = r * p.gp_magic >> 16, tk = it.tok0 + rl, h = it.g0 + (r - rl * p.GP);
+                        if (tk >= p.T || h >= p.G) continue;
+                        if (poison && tk < it.fresh) add_not_finite(v, 4, c0 + c4, tk);
                         if (it.whole)
                             *reinterpret_cast<uint2 *>(out_row(h, tk) + c0 + c4) =
                                 make_uint2(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]));
                         else
                             *reinterpret_cast<float4 *>(p.part_o + (prow0 + r) * D + c0 + c4) =
                                 make_float4(v[0], v[1], v[2], v[3]);
-                        if (c0 == 0 && c4 == 0) {
-                            if (it.whole)
-                                p.lse[((long long)it.b * p.Hk * p.G + it.hk * p.G + h) * p.T + tk] =
-                                    ls2 * 0.69314718055994531f;
-                            else
-                                p.part_lse[prow0 + r] = ls2;
-                        }
                     }
                 }
+            }
+            if (mine && kw == 0) {
+                if (it.whole)
+                    p.lse[((long long)it.b * p.Hk * p.G + it.hk * p.G + head) * p.T + tok] =
+                        lse2 * 0.69314718055994531f;
+                else
+                    p.part_lse[prow0 + row] = lse2;
             }
             gj += nt;
             if (nt > 0) ++t;
         }
     } else {
         // ------------------------------ pieces of work ----------------------------------
-        if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (blockIdx.x == 0)
             for (int b = lane; b < p.B; b += 32) page_lengths_check(p.pt, p.T, b);
         paged_walk<RT>(p, bars, lane);
