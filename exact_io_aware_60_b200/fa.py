@@ -489,16 +489,49 @@ def rope_plan(rot_dim: int, *, layout: str = "half", base: float = 10000.0, scal
 
 
 _I3 = ctypes.c_longlong * 3
+_CODES = {torch.bfloat16: FA_BF16, torch.float16: FA_FP16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (no Stream object made)
 
 
-def _rows(t, name: str, shape, dtype, device):
+def _stream_of(index: int, stream) -> int:
+    """The caller's stream, or device ``index``'s current one."""
+    if stream is not None:
+        return int(stream.cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(index)
+    return int(torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on_device(index: int, fn, args):
+    """``fn(*args)`` with the tensors' device current (it makes no difference to the caller's)."""
+    before = torch.cuda.current_device()
+    if before == index:
+        return fn(*args)
+    torch.cuda.set_device(index)
+    try:
+        return fn(*args)
+    finally:
+        torch.cuda.set_device(before)
+
+
+def _main(t, name: str):
+    """(shape, dtype, device index, dtype code) of a call's first tensor, [.., .., .., d]."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
+        raise FAError(FA_ERR_INVALID_ARG, f"{name} must be a 4-dimensional CUDA tensor")
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise FAError(FA_ERR_INVALID_ARG, f"unsupported dtype {t.dtype}")
+    return t.shape, t.dtype, t.get_device(), code
+
+
+def _rows(t, name: str, shape, dtype, index: int):
     """Checks a [.., .., .., d] tensor with d contiguous; its strides for the library (None if
     contiguous)."""
     if not isinstance(t, torch.Tensor):
         raise FAError(FA_ERR_INVALID_ARG, f"{name} must be a torch.Tensor")
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
         raise FAError(FA_ERR_INVALID_ARG,
-                      f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} "
+                      f"{name}: expected {dtype} {tuple(shape)} on cuda:{index}, got {t.dtype} "
                       f"{tuple(t.shape)} on {t.device}")
     if t.is_contiguous():
         return None
@@ -508,72 +541,51 @@ def _rows(t, name: str, shape, dtype, device):
     return _I3(st[0], st[1], st[2])
 
 
-def _ints(t, name: str, shapes, device, dtype=torch.int32):
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device \
-            or tuple(t.shape) not in shapes or not t.is_contiguous():
+def _ints(t, name: str, shapes, index: int, dtype=torch.int32):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index \
+            or t.shape not in shapes or not t.is_contiguous():
         raise FAError(FA_ERR_INVALID_ARG,
-                      f"{name} must be a contiguous {dtype} tensor on {device}, shape "
+                      f"{name} must be a contiguous {dtype} tensor on cuda:{index}, shape "
                       + " or ".join(str(s) for s in shapes))
     return t.data_ptr()
 
 
-def _main(t, name: str) -> torch.device:
-    """The device of a call: that of its first tensor, [.., .., .., d] bf16 or fp16."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
-        raise FAError(FA_ERR_INVALID_ARG, f"{name} must be a 4-dimensional CUDA tensor")
-    return t.device
-
-
-class _On:
-    """The call's device and stream: the tensors' device is made current for the call, and the
-    stream is that device's current one unless the caller gives another."""
-    __slots__ = ("index", "before", "stream")
-
-    def __init__(self, device, stream):
-        self.index, self.stream = device.index, stream
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-        return _stream_handle(self.stream)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
-        return False
-
-
-def _plan_args(plan, device):
+def _plan_args(plan, index: int):
     if not isinstance(plan, RopePlan):
         raise FAError(FA_ERR_INVALID_ARG, "the rotation must be a RopePlan (see rope_plan)")
-    _ints(plan.turns, "plan.turns", ((plan.rot_dim // 2,),), device, torch.int64)
-    return plan.turns.data_ptr(), plan.rot_dim, int(plan.interleaved), plan.magnitude
+    turns = _ints(plan.turns, "plan.turns", ((plan.rot_dim // 2,),), index, torch.int64)
+    return turns, plan.rot_dim, int(plan.interleaved), plan.magnitude
 
 
 def _rope_call(fn, where, x, x_out, plan, y, y_out, positions, stream, names):
-    device = _main(x, names[0])
-    B, H, N, d = x.shape
-    xs = _rows(x, names[0], x.shape, x.dtype, device)
-    xos = _rows(x_out, names[1], x.shape, x.dtype, device)
-    if (y is None) != (y_out is None):
-        raise FAError(FA_ERR_INVALID_ARG, f"{names[2]} and {names[3]} go together")
+    shape, dtype, index, code = _main(x, names[0])
+    B, H, N, d = shape
+    xs = None if x.is_contiguous() else _rows(x, names[0], shape, dtype, index)
+    xos = _rows(x_out, names[1], shape, dtype, index)
     yp = yop = ys = yos = None
     Hk = 0
     if y is not None:
-        Hk = y.shape[1] if isinstance(y, torch.Tensor) and y.dim() == 4 else 0
-        shape = torch.Size((B, Hk, N, d))
-        ys = _rows(y, names[2], shape, x.dtype, device)
-        yos = _rows(y_out, names[3], shape, x.dtype, device)
+        if not isinstance(y, torch.Tensor) or y.dim() != 4 or y_out is None:
+            raise FAError(FA_ERR_INVALID_ARG, f"{names[2]} and {names[3]} go together, both "
+                                              "4-dimensional tensors")
+        ysh = y.shape
+        Hk = ysh[1]
+        if ysh != (B, Hk, N, d):
+            raise FAError(FA_ERR_INVALID_ARG, f"{names[2]}: expected {(B, 'Hk', N, d)}, got "
+                                              f"{tuple(ysh)}")
+        ys = _rows(y, names[2], ysh, dtype, index)
+        yos = _rows(y_out, names[3], ysh, dtype, index)
         yp, yop = y.data_ptr(), y_out.data_ptr()
+    elif y_out is not None:
+        raise FAError(FA_ERR_INVALID_ARG, f"{names[2]} and {names[3]} go together")
     pp, per_batch = None, 0
     if positions is not None:
-        pp = _ints(positions, "positions", ((N,), (B, N)), device)
-        per_batch = int(positions.dim() == 2)
-    turns, rot, inter, mag = _plan_args(plan, device)
-    with _On(device, stream) as st:
-        rc = fn(x.data_ptr(), x_out.data_ptr(), yp, yop, B, H, Hk, N, d, xs, xos, ys, yos, pp,
-                per_batch, turns, rot, inter, mag, _dtype_code(x), st)
+        pp = _ints(positions, "positions", ((N,), (B, N)), index)
+        per_batch = positions.dim() - 1
+    turns, rot, inter, mag = _plan_args(plan, index)
+    rc = _on_device(index, fn, (x.data_ptr(), x_out.data_ptr(), yp, yop, B, H, Hk, N, d, xs, xos,
+                                ys, yos, pp, per_batch, turns, rot, inter, mag, code,
+                                _stream_of(index, stream)))
     if rc != FA_OK:
         raise FAError(rc, where)
 
@@ -582,7 +594,7 @@ def fa_rope(q, q_out, plan: RopePlan, *, k=None, k_out=None, positions=None, str
     """Rotary positions: writes ``q_out`` [B,H,N,d] (and ``k_out`` [B,Hk,N,d]) from ``q`` (and
     ``k``) in one launch; ``q_out`` may be ``q``.  Strided views with a contiguous last
     dimension are taken as they are.  ``positions``: int32 [N] or [B,N], None for 0 .. N-1."""
-    _rope_call(lib().fa_rope, "fa_rope", q, q_out, plan, k, k_out, positions, stream,
+    _rope_call((_lib or lib()).fa_rope, "fa_rope", q, q_out, plan, k, k_out, positions, stream,
                ("q", "q_out", "k", "k_out"))
 
 
@@ -590,28 +602,29 @@ def fa_rope_bwd(dq_rot, dq, plan: RopePlan, *, k=None, k_out=None, positions=Non
                 stream=None) -> None:
     """Backward pass of :func:`fa_rope`: gradients of its inputs from those of its outputs.
     ``dq_rot`` -> ``dq``, and ``k`` (the gradient of the rotated keys) -> ``k_out``."""
-    _rope_call(lib().fa_rope_bwd, "fa_rope_bwd", dq_rot, dq, plan, k, k_out, positions, stream,
+    _rope_call((_lib or lib()).fa_rope_bwd, "fa_rope_bwd", dq_rot, dq, plan, k, k_out, positions, stream,
                ("dq_rot", "dq", "k", "k_out"))
 
 
 # ------------------------------------------------------------------ paged cache
 
-def _cache_args(k_cache, v_cache, block_table, cache_len, new_len, B, Hk, d, dtype, device):
+def _cache_args(k_cache, v_cache, block_table, cache_len, new_len, B, Hk, d, dtype, index):
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise FAError(FA_ERR_INVALID_ARG, "k_cache must be a [pages, Hk, page_size, d] tensor")
-    P, hk, page, dc = k_cache.shape
-    if hk != Hk or dc != d:
-        raise FAError(FA_ERR_INVALID_ARG, f"k_cache: expected [pages, {Hk}, page_size, {d}], got "
-                                          f"{tuple(k_cache.shape)}")
-    ks = _rows(k_cache, "k_cache", k_cache.shape, dtype, device)
-    vs = _rows(v_cache, "v_cache", k_cache.shape, dtype, device)
+    shape = k_cache.shape
+    P, hk, page, dc = shape
+    if (Hk and hk != Hk) or dc != d:
+        raise FAError(FA_ERR_INVALID_ARG, f"k_cache: expected [pages, {Hk or 'Hk'}, page_size, {d}], "
+                                          f"got {tuple(shape)}")
+    ks = _rows(k_cache, "k_cache", shape, dtype, index)
+    vs = _rows(v_cache, "v_cache", shape, dtype, index)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise FAError(FA_ERR_INVALID_ARG, "block_table must be an int32 [B, max_blocks] tensor")
     blocks = block_table.shape[1]
-    table = _ints(block_table, "block_table", ((B, blocks),), device)
-    held = _ints(cache_len, "cache_len", ((B,),), device)
-    new = None if new_len is None else _ints(new_len, "new_len", ((B,),), device)
-    return ks, vs, P, page, table, blocks, held, new
+    table = _ints(block_table, "block_table", ((B, blocks),), index)
+    held = _ints(cache_len, "cache_len", ((B,),), index)
+    new = None if new_len is None else _ints(new_len, "new_len", ((B,),), index)
+    return ks, vs, P, hk, page, table, blocks, held, new
 
 
 def fa_kv_append(k, v, k_cache, v_cache, block_table, cache_len, *, new_len=None,
@@ -622,28 +635,32 @@ def fa_kv_append(k, v, k_cache, v_cache, block_table, cache_len, *, new_len=None
     of sequence b goes to slot ``cache_len[b] + t`` (see include/fa.h); the lengths are not
     advanced.  ``new_len``: int32 [B], None for T each; ``positions``: int32 [B,T], None for
     the slots' own.  Strided views with a contiguous last dimension are taken as they are."""
-    device = _main(k, "k")
-    B, Hk, T, d = k.shape
-    ks = _rows(k, "k", k.shape, k.dtype, device)
-    vs = _rows(v, "v", k.shape, k.dtype, device)
-    kcs, vcs, P, page, table, blocks, held, new = _cache_args(
-        k_cache, v_cache, block_table, cache_len, new_len, B, Hk, d, k.dtype, device)
-    if (q is None) != (q_out is None):
-        raise FAError(FA_ERR_INVALID_ARG, "q and q_out go together")
+    shape, dtype, index, code = _main(k, "k")
+    B, Hk, T, d = shape
+    ks = None if k.is_contiguous() else _rows(k, "k", shape, dtype, index)
+    vs = _rows(v, "v", shape, dtype, index)
+    kcs, vcs, P, _, page, table, blocks, held, new = _cache_args(
+        k_cache, v_cache, block_table, cache_len, new_len, B, Hk, d, dtype, index)
     qp = qop = qs = qos = None
     H = 0
     if q is not None:
-        H = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 4 else 0
-        shape = torch.Size((B, H, T, d))
-        qs = _rows(q, "q", shape, k.dtype, device)
-        qos = _rows(q_out, "q_out", shape, k.dtype, device)
+        if not isinstance(q, torch.Tensor) or q.dim() != 4 or q_out is None:
+            raise FAError(FA_ERR_INVALID_ARG, "q and q_out go together, both 4-dimensional tensors")
+        qsh = q.shape
+        H = qsh[1]
+        if qsh != (B, H, T, d):
+            raise FAError(FA_ERR_INVALID_ARG, f"q: expected {(B, 'H', T, d)}, got {tuple(qsh)}")
+        qs = _rows(q, "q", qsh, dtype, index)
+        qos = _rows(q_out, "q_out", qsh, dtype, index)
         qp, qop = q.data_ptr(), q_out.data_ptr()
-    pp = None if positions is None else _ints(positions, "positions", ((B, T),), device)
-    turns, rot, inter, mag = (None, 0, 0, 1.0) if rope is None else _plan_args(rope, device)
-    with _On(device, stream) as st:
-        rc = lib().fa_kv_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                qp, qop, B, H, Hk, T, d, ks, vs, qs, qos, kcs, vcs, P, page, table,
-                                blocks, held, new, pp, turns, rot, inter, mag, _dtype_code(k), st)
+    elif q_out is not None:
+        raise FAError(FA_ERR_INVALID_ARG, "q and q_out go together")
+    pp = None if positions is None else _ints(positions, "positions", ((B, T),), index)
+    turns, rot, inter, mag = (None, 0, 0, 1.0) if rope is None else _plan_args(rope, index)
+    rc = _on_device(index, (_lib or lib()).fa_kv_append, (
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), qp, qop, B, H, Hk, T, d,
+        ks, vs, qs, qos, kcs, vcs, P, page, table, blocks, held, new, pp, turns, rot, inter, mag,
+        code, _stream_of(index, stream)))
     if rc != FA_OK:
         raise FAError(rc, "fa_kv_append")
 
@@ -658,26 +675,25 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, cache_len, o, lse, *, scale: 
     keys and values: writes ``o`` [B,H,T,d] and ``lse`` [B,H,T].  ``tree_mask``: uint8 [T,T] or
     [B,T,T] (row = token, column = new key it sees), None for a chain.  ``workspace``: uint8
     CUDA tensor of ``fa_fwd_paged_workspace_bytes`` bytes.  See include/fa.h."""
-    device = _main(q, "q")
-    B, H, T, d = q.shape
-    qs = _rows(q, "q", q.shape, q.dtype, device)
-    os_ = _rows(o, "o", q.shape, q.dtype, device)
-    Hk = k_cache.shape[1] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else 0
-    kcs, vcs, P, page, table, blocks, held, new = _cache_args(
-        k_cache, v_cache, block_table, cache_len, new_len, B, Hk, d, q.dtype, device)
-    lp = _ints(lse, "lse", ((B, H, T),), device, torch.float32)
+    shape, dtype, index, code = _main(q, "q")
+    B, H, T, d = shape
+    qs = None if q.is_contiguous() else _rows(q, "q", shape, dtype, index)
+    os_ = _rows(o, "o", shape, dtype, index)
+    kcs, vcs, P, Hk, page, table, blocks, held, new = _cache_args(
+        k_cache, v_cache, block_table, cache_len, new_len, B, 0, d, dtype, index)
+    lp = _ints(lse, "lse", ((B, H, T),), index, torch.float32)
     tp, per_batch = None, 0
     if tree_mask is not None:
-        tp = _ints(tree_mask, "tree_mask", ((T, T), (B, T, T)), device, torch.uint8)
-        per_batch = int(tree_mask.dim() == 3)
-    if not isinstance(workspace, torch.Tensor) or workspace.device != device \
-            or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
-        raise FAError(FA_ERR_INVALID_ARG, f"workspace must be a contiguous uint8 tensor on {device}")
-    with _On(device, stream) as st:
-        rc = lib().fa_fwd_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
-                                lp, B, H, Hk, T, d, qs, os_, kcs, vcs, P, page, table, blocks,
-                                held, new, tp, per_batch, float(scale), _dtype_code(q),
-                                workspace.data_ptr(), workspace.numel(), st)
+        tp = _ints(tree_mask, "tree_mask", ((T, T), (B, T, T)), index, torch.uint8)
+        per_batch = tree_mask.dim() - 2
+    if not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 \
+            or workspace.get_device() != index or not workspace.is_contiguous():
+        raise FAError(FA_ERR_INVALID_ARG,
+                      f"workspace must be a contiguous uint8 tensor on cuda:{index}")
+    rc = _on_device(index, (_lib or lib()).fa_fwd_paged, (
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), lp, B, H, Hk, T, d, qs,
+        os_, kcs, vcs, P, page, table, blocks, held, new, tp, per_batch, float(scale), code,
+        workspace.data_ptr(), workspace.numel(), _stream_of(index, stream)))
     if rc != FA_OK:
         raise FAError(rc, "fa_fwd_paged")
 
@@ -741,7 +757,8 @@ def backward(q, k, v, o, dout, lse, *, scale: Optional[float] = None, causal: bo
 def _allocating(t, name: str, stream):
     """The helpers below allocate on the tensors' device and in the call's stream, so that a
     temporary's memory is reused only after the kernels that still read it."""
-    with _On(_main(t, name), stream):
+    _main(t, name)
+    with torch.cuda.device(t.get_device()):
         if stream is None:
             yield
         else:
