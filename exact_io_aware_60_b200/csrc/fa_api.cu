@@ -860,7 +860,7 @@ bool make_query_map(CUtensorMap *m, const fa::Rows &r, int bf16, int d, int H, i
 
 template <int D, bool BF16, int REP, int RT>
 int launch_paged(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
-                 const fa::PagedParams &p, int cap_tiles, cudaStream_t st, int dev) {
+                 const fa::PagedParams &p, cudaStream_t st, int dev) {
     using C = fa::PagedCfg<D, REP, RT>;
     auto kern = fa::fa_paged_kernel<D, BF16, REP, RT>;
     static std::atomic<int> smem_done[kMaxDevices];
@@ -870,12 +870,13 @@ int launch_paged(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap
         return FA_ERR_CUDA;
     }
     e = launch_pdl(kern, dim3((unsigned)p.ctas), dim3(C::THREADS), C::SMEM, st, mq, mk, mv, p);
-    if (e == cudaSuccess && cap_tiles > 1) {
+    if (e == cudaSuccess && !p.uncut) {
+        constexpr bool TRANS = REP == 1;
         // rows in use: all of an item's, or those of the call's tokens where these are fewer
-        const int rows = RT == 2 ? 256 : std::min(p.TPT, p.T) * p.GP;
-        e = launch_pdl(fa::fa_paged_merge_kernel<D, BF16, RT>,
-                       dim3((unsigned)(p.B * p.Hk * p.row_tiles), (unsigned)((rows + 3) / 4)),
-                       dim3(128), 0, st, p, (int)C::ROWS);
+        const int rows = RT == 2 ? 256 : std::min(p.TPT, p.T) * p.GP, per = TRANS ? 32 : 16;
+        e = launch_pdl(fa::fa_paged_merge_kernel<D, BF16, RT, TRANS>,
+                       dim3((unsigned)(p.B * p.Hk * p.row_tiles), (unsigned)((rows + per - 1) / per)),
+                       dim3(256), 0, st, p, (int)C::ROWS);
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
@@ -1337,6 +1338,8 @@ int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *
     p.gp_magic = (65536u + sh.GP - 1) / sh.GP;
     p.GT = sh.GT;
     p.TPT = sh.TPT;
+    // Up to four tiles an item are not cut: a tile more takes about 1 us, the merge 3 us.
+    p.uncut = cap_tiles <= 4;
     p.row_tiles = (int)sh.row_tiles;
     p.ctas = (int)std::min<double>(ctas, (double)sh.row_tiles * Hk * B * cap_tiles);
     p.scale_log2 = scale * 1.4426950408889634f;
@@ -1348,7 +1351,7 @@ int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *
         !make_cache_map(&mv, p.vc, bf16, d, page_size, Hk, num_pages, box_rows))
         return FA_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-#define FA_PAGED_ARGS mq, mk, mv, p, (int)cap_tiles, st, dev
+#define FA_PAGED_ARGS mq, mk, mv, p, st, dev
 #define FA_PAGED(D, BF) (sh.rows == 32    ? launch_paged<D, BF, 4, 1>(FA_PAGED_ARGS) \
                          : sh.rows == 64  ? launch_paged<D, BF, 2, 1>(FA_PAGED_ARGS) \
                          : sh.rows == 128 ? launch_paged<D, BF, 1, 1>(FA_PAGED_ARGS) \

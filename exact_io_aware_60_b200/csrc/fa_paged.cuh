@@ -19,9 +19,11 @@
 // launched early by PDL, merges them in a fixed order.
 //
 // CTA: softmax warps (one row per thread, 4 per row tile), then one producer warp (page table
-// and TMA of K and V), one MMA issuer, one that loads Q and repairs V tiles (see repair), and
-// one that works out the CTA's pieces of work ahead of the others and hands them over in
-// shared memory (its lookups of lengths, about 1 us an item, are off everybody's path).
+// and TMA of K and V), one issuer of S, one of P V, and one that works out the CTA's pieces of
+// work two ahead of the others (its lookups of lengths, about 1 us an item, are off everybody's
+// path), loads Q and repairs V tiles (see repair).  Two issuers, because a commit leaves the
+// tensor core idle for about 150 cycles in the stream of one: S and P V of 128 keys x 128 rows
+// at d = 128, committed each, took 1330 cycles from one thread and 1075 from two.
 //
 // Few rows (REP = 4: a tile of 32 rows, REP = 2: 64): the rows are repeated in the tile's
 // REP lane quarters / halves, and each copy takes 1 / REP of the keys of every tile as a
@@ -52,6 +54,7 @@ struct PagedParams {
     int GP, GT;          // heads of a row tile; row tiles that a token's G heads take (1 up to
                          // 128 heads to a key/value head)
     int TPT;             // tokens of a row tile: (rows of a tile) / GP
+    int uncut;           // items are not cut: a share is a number of whole items
     int row_tiles;       // items of a (sequence, key/value head): ceil(T / (TPT * RT)) * GT
     int ctas;            // shares
     float scale_log2;
@@ -67,8 +70,9 @@ struct PagedCfg {
     static constexpr int TILE = BN * D * 2;     // K or V tile
     static constexpr int HALF = BN * 128;       // one 64-element column block of a tile
     static constexpr int NS = (D == 64) ? (RT == 1 ? 11 : 10) : (RT == 1 ? 5 : 4);  // K, V ring
-    // REP merge: a 32-column block of every row and copy, rows padded to 36 columns
-    static constexpr int MERGE = (REP > 1) ? 128 * 36 * 4 : 0;
+    // epilogue: REP > 1, a 32-column block of every row and copy, rows padded to 36 columns;
+    // else 32 rows x 32 columns of 16 bits for each warp
+    static constexpr int MERGE = (REP > 1) ? 128 * 36 * 4 : RT * 4 * 2048;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + RT * QTILE;
     static constexpr int OFF_MERGE = OFF_RING + NS * TILE;
@@ -77,12 +81,15 @@ struct PagedCfg {
     static constexpr int SMEM = USED + 1024;
     static constexpr int SOFT = 4 * RT;         // softmax warps
     static constexpr int THREADS = 32 * (SOFT + 4);
-    // TMEM: two score buffers (RT = 1: alternating tiles; RT = 2: one per row tile).  P has
-    // columns of its own except at d = 128 with two row tiles, where it overwrites S.
-    static constexpr bool P_OWN = !(D == 128 && RT == 2);
+    // The softmax goes in steps of a whole tile (RT = 1) or 64 keys (RT = 2).  TMEM: two
+    // score buffers per row tile in turn, so that a step's S is there before the last step's
+    // P V is; P has columns of its own (RT = 1) or overwrites S.
+    static constexpr int SPT = RT;              // steps of a tile
+    static constexpr int STEP = BN / SPT;       // keys of a step
+    static constexpr bool P_OWN = RT == 1;
     static constexpr uint32_t COL_S = 0;
     static constexpr uint32_t COL_P = P_OWN ? 256 : 0;
-    static constexpr uint32_t P_STEP = P_OWN ? 64 : 128;
+    static constexpr uint32_t P_STEP = 64;      // between the two buffers of P
     static constexpr uint32_t COL_O = P_OWN ? 384 : 256;
     static_assert(COL_O + RT * D <= 512, "TMEM budget");
     static_assert(SMEM <= 232448, "shared memory budget");
@@ -91,13 +98,17 @@ struct PagedCfg {
 struct PagedBars {
     uint64_t q_full, q_empty, o_empty;
     // The MMA issuer asks for the repair of a tile's V once the tile's S is issued: from then
-    // on the V slot's fill is the next or the last one, so that the parity that the repairing
-    // warp waits for is unambiguous.  (Two, alternating: a request may be made while the one
-    // before it is not yet served.)
-    uint64_t need[2];
-    // index: RT = 1 the tile's parity, RT = 2 the row tile
-    uint64_t s_full[2], s_empty[2], p_full[2], pv_done[2];
-    uint64_t full[12], empty[12], fixed[12];  // per ring slot; fixed: V repaired
+    // on the tile's vfull phase is the current or the last one, so that the parity that the repairing
+    // warp waits for is unambiguous.  (Four in turn: S runs at most four tiles ahead of a
+    // repair, as P V of the first waits for it.)
+    uint64_t need[4];
+    // index: 2 * row tile + the step's parity
+    uint64_t s_full[4], s_empty[4], p_full[4], pv_done[4];
+    // Fills are announced per tile (mod 8; a ring holds at most 6), K and V apart, so that
+    // each is waited for in order by the issuer that uses it; a ring slot, which K and V may
+    // take in turn, is released per slot.  fixed: V repaired.
+    uint64_t kfull[8], vfull[8], fixed[8];
+    uint64_t empty[12];
     uint64_t seg_full[4], seg_empty[4];
     uint32_t tmem_base;
     int4 seg[4][3];         // ring of pieces (PagedSeg)
@@ -123,7 +134,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams &p, int b) {
     page_lengths(p.pt, p.T, b, s.past, s.fresh);
     s.tiles = (s.past + s.fresh + 127) >> 7;
     s.valid = (s.fresh + p.TPT * RT - 1) / (p.TPT * RT) * p.GT;
-    s.per_head = s.valid * (s.tiles + kItemCost) + (p.row_tiles - s.valid);
+    s.per_head = p.uncut ? p.row_tiles : s.valid * (s.tiles + kItemCost) + (p.row_tiles - s.valid);
     return s;
 }
 
@@ -184,40 +195,96 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
     return __vcmpeq2(w & e, e);
 }
 
-// Hands this CTA's pieces over, in order (one whole warp; the lanes share the lookups).
+// Works out this CTA's pieces, in order (one whole warp; the lanes share the lookups: a group
+// of 32 sequences, one per lane), and hands them over.
 template <int RT>
-__device__ __forceinline__ void paged_walk(const PagedParams &p, PagedBars *bars, int lane) {
-    // lengths of up to 32 sequences at a time, one per lane
-    int W = 0, k0 = 0, mine;
+struct PagedWalk {
+    int u, u1;          // the share's next unit, its end
+    int k0, base;       // the group with unit u, the units before it
+    int mine, upto;     // units of the lane's sequence, sums up to it
     PagedSeq sq;
-    auto load = [&](int k) {
+    int n;              // pieces handed over
+    bool first, done;
+
+    __device__ __forceinline__ void load(const PagedParams &p, int k, int lane) {
+        k0 = k;
         mine = 0;
         if (k + lane < p.B) {
             sq = paged_seq<RT>(p, k + lane);
             mine = sq.per_head * p.Hk;
         }
-    };
-    for (int k = 0; k < p.B; k += 32) {
-        load(k);
-        W += warp_sum(mine);
     }
-    PagedShares sh;
-    sh.init(W, p.ctas);
-    const int c = blockIdx.x;
-    int u = min(sh.begin(c), W);
-    const int u1 = min(sh.begin(c + 1), W);
-    // the group of sequences with unit u
-    int base = 0, upto = 0;  // units before the group; inclusive sums within it
-    if (p.B > 32) load(0);
-    for (; u < u1; k0 += 32) {
+    __device__ __forceinline__ void init(const PagedParams &p, int lane) {
+        int W = 0;
+        for (int k = 0; k < p.B; k += 32) {
+            load(p, k, lane);
+            W += warp_sum(mine);
+        }
+        PagedShares sh;
+        sh.init(W, p.ctas);
+        u = min(sh.begin(blockIdx.x), W);
+        u1 = min(sh.begin(blockIdx.x + 1), W);
+        if (p.B > 32) load(p, 0, lane);
+        base = 0;
         upto = warp_scan(mine, lane);
-        const int all = __shfl_sync(0xffffffffu, upto, 31);
-        if (base + all > u) break;
-        base += all;
-        load(k0 + 32);
+        n = 0;
+        first = true;
+        done = false;
     }
-    int n = 0;
-    auto put = [&](const PagedSeg &g) -> bool {
+    // The next piece goes to the ring (b = -1 after the last); false if a wait gave up.
+    __device__ __forceinline__ bool step(const PagedParams &p, PagedBars *bars, int lane) {
+        if (done) return true;
+        PagedSeg g;
+        g.b = -1;
+        while (u < u1) {
+            for (int all; base + (all = __shfl_sync(0xffffffffu, upto, 31)) <= u;) {
+                base += all;
+                load(p, k0 + 32, lane);
+                upto = warp_scan(mine, lane);
+            }
+            const int f = __ffs(__ballot_sync(0xffffffffu, base + upto > u)) - 1;
+            const int r0 = u - base - __shfl_sync(0xffffffffu, upto - mine, f);
+            const int per_head = __shfl_sync(0xffffffffu, sq.per_head, f);
+            const int tiles = __shfl_sync(0xffffffffu, sq.tiles, f);
+            const int valid = __shfl_sync(0xffffffffu, sq.valid, f);
+            g.past = __shfl_sync(0xffffffffu, sq.past, f);
+            g.fresh = __shfl_sync(0xffffffffu, sq.fresh, f);
+            g.total = g.past + g.fresh;
+            g.hk = (unsigned)r0 / (unsigned)per_head;
+            const int r = r0 - g.hk * per_head;
+            const int cost = tiles + kItemCost;
+            g.slot = 2 * blockIdx.x + (first ? 0 : 1);
+            first = false;
+            int rt;
+            if (p.uncut) {
+                rt = r;
+                g.j0 = 0;
+                g.j1 = rt < valid ? tiles : 0;
+                g.whole = 1;
+                u += 1;
+            } else if (r < valid * cost) {
+                rt = (unsigned)r / (unsigned)cost;
+                g.j0 = min(r - rt * cost, tiles);
+                const int end = min(cost, r - rt * cost + (u1 - u));
+                g.j1 = min(end, tiles);
+                u += end - (r - rt * cost);
+                if (g.j0 == g.j1) continue;  // nothing but the item's own cost
+                g.whole = g.j0 == 0 && g.j1 == tiles;
+            } else {
+                rt = valid + (r - valid * cost);
+                g.j0 = g.j1 = 0;
+                g.whole = 1;
+                u += 1;
+            }
+            g.b = k0 + f;
+            const int tt = p.GT == 1 ? rt : rt / p.GT;
+            g.tok0 = tt * RT * p.TPT;
+            g.g0 = p.GT == 1 ? 0 : (rt - tt * p.GT) * p.GP;
+            if (p.tree == nullptr)  // a chain's rows see no key behind their last token
+                g.j1 = min(g.j1, (g.past + min(g.fresh, g.tok0 + RT * p.TPT) + 127) >> 7);
+            break;
+        }
+        done = g.b < 0;
         if (n >= 4 && !__all_sync(0xffffffffu, mbar_wait(&bars->seg_empty[n & 3], ((n >> 2) - 1) & 1)))
             return false;
         if (lane == 0) {
@@ -230,57 +297,8 @@ __device__ __forceinline__ void paged_walk(const PagedParams &p, PagedBars *bars
         __syncwarp();
         ++n;
         return true;
-    };
-    PagedSeg g;
-    bool first = true;
-    while (u < u1) {
-        while (true) {  // the group with unit u
-            const int all = __shfl_sync(0xffffffffu, upto, 31);
-            if (base + all > u) break;
-            base += all;
-            k0 += 32;
-            load(k0);
-            upto = warp_scan(mine, lane);
-        }
-        const int f = __ffs(__ballot_sync(0xffffffffu, base + upto > u)) - 1;
-        const int r0 = u - base - __shfl_sync(0xffffffffu, upto - mine, f);
-        const int per_head = __shfl_sync(0xffffffffu, sq.per_head, f);
-        const int tiles = __shfl_sync(0xffffffffu, sq.tiles, f);
-        const int valid = __shfl_sync(0xffffffffu, sq.valid, f);
-        g.b = k0 + f;
-        g.past = __shfl_sync(0xffffffffu, sq.past, f);
-        g.fresh = __shfl_sync(0xffffffffu, sq.fresh, f);
-        g.total = g.past + g.fresh;
-        g.hk = (unsigned)r0 / (unsigned)per_head;
-        const int r = r0 - g.hk * per_head;
-        const int cost = tiles + kItemCost;
-        g.slot = 2 * c + (first ? 0 : 1);
-        first = false;
-        int rt;
-        if (r < valid * cost) {
-            rt = (unsigned)r / (unsigned)cost;
-            g.j0 = min(r - rt * cost, tiles);
-            const int end = min(cost, r - rt * cost + (u1 - u));
-            g.j1 = min(end, tiles);
-            u += end - (r - rt * cost);
-            if (g.j0 == g.j1) continue;  // nothing but the item's own cost
-            g.whole = g.j0 == 0 && g.j1 == tiles;
-        } else {
-            rt = valid + (r - valid * cost);
-            g.j0 = g.j1 = 0;
-            g.whole = 1;
-            u += 1;
-        }
-        const int tt = p.GT == 1 ? rt : rt / p.GT;
-        g.tok0 = tt * RT * p.TPT;
-        g.g0 = p.GT == 1 ? 0 : (rt - tt * p.GT) * p.GP;
-        if (p.tree == nullptr)  // a chain's rows see no key behind their last token
-            g.j1 = min(g.j1, (g.past + min(g.fresh, g.tok0 + RT * p.TPT) + 127) >> 7);
-        if (!put(g)) return;
     }
-    g.b = -1;
-    put(g);
-}
+};
 
 // Takes piece n (all lanes that use it; lane 0 among them); false after the last one, or when
 // the wait gave up.
@@ -306,6 +324,10 @@ __device__ __forceinline__ void tma_load_4d(void *smem_dst, const void *tmap, ui
         " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 // C columns of 32 TMEM lanes.
@@ -356,8 +378,9 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedParams p) {
     using C = PagedCfg<D, REP, RT>;
     constexpr int ROWS = C::ROWS;
-    constexpr int CW = 128 / REP;     // keys of a tile that one thread handles
-    constexpr int W_TMA = C::SOFT, W_MMA = C::SOFT + 1, W_FIX = C::SOFT + 2, W_WALK = C::SOFT + 3;
+    constexpr int CW = C::STEP / REP; // keys of a step that one thread handles
+    constexpr int SPT = C::SPT;
+    constexpr int W_TMA = C::SOFT, W_S = C::SOFT + 1, W_PV = C::SOFT + 2, W_FIX = C::SOFT + 3;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sQ = smem + C::OFF_Q;
@@ -367,34 +390,33 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
-    // Barrier index and phase of tile g (RT = 1: two alternating buffers; RT = 2: row tile i
-    // has one).
-    auto bi = [](int g, int i) { return RT == 1 ? (g & 1) : i; };
-    auto ph = [](int g) { return RT == 1 ? ((g >> 1) & 1) : (g & 1); };
-    constexpr int BUFS = RT == 1 ? 2 : 1;  // tiles between two uses of a buffer
+    // Barrier index and phase of step n, row tile i.
+    auto bi = [](int n, int i) { return 2 * i + (n & 1); };
+    auto ph = [](int n) { return (n >> 1) & 1; };
 
-    if (threadIdx.x == W_MMA * 32) {
+    if (threadIdx.x == W_S * 32) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
         mbar_init(&bars->q_full, 1);
         mbar_init(&bars->q_empty, 1);
         mbar_init(&bars->o_empty, 128 * RT);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->need[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&bars->need[i], 1);
+        for (int i = 0; i < 2 * RT; ++i) {
             mbar_init(&bars->s_full[i], 1);
             mbar_init(&bars->s_empty[i], 128);
             mbar_init(&bars->p_full[i], 128);
             mbar_init(&bars->pv_done[i], 1);
         }
-        for (int i = 0; i < C::NS; ++i) {
-            mbar_init(&bars->full[i], 1);
-            mbar_init(&bars->empty[i], 1);
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&bars->kfull[i], 1);
+            mbar_init(&bars->vfull[i], 1);
             mbar_init(&bars->fixed[i], 1);
         }
+        for (int i = 0; i < C::NS; ++i) mbar_init(&bars->empty[i], 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars->seg_full[i], 1);
-            mbar_init(&bars->seg_empty[i], C::SOFT + 3);
+            mbar_init(&bars->seg_empty[i], C::SOFT + 4);
         }
         fence_mbar_init();
     }
@@ -402,6 +424,12 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (warp == W_FIX) {  // (hints only: nothing is read before the wait)
+        for (int b = lane * 32; b < p.B; b += 1024) {
+            prefetch_l2(p.pt.cache_len + b);
+            if (p.pt.new_len) prefetch_l2(p.pt.new_len + b);
+        }
+    }
     pdl_wait();
     pdl_launch_dependents();
     const uint32_t tmem = bars->tmem_base;
@@ -416,7 +444,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const int box_rows = min(page, 128);
         const int npt = 128 / box_rows;
         const int mine = lane % npt, half = lane / npt;
-        int gj = 0;  // tiles so far
+        int gj = 0, fills = 0;  // tiles and fills so far
         bool ok = true;
         while (ok && paged_take(bars, np++, lane, true, it)) {
             const int *row = p.pt.table + (long long)it.b * p.pt.max_blocks;
@@ -441,102 +469,119 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     if (n >= C::NS)
                         ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[s], (n / C::NS - 1) & 1));
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&bars->full[s], C::TILE);
+                    uint64_t *full = kv ? &bars->vfull[gj & 7] : &bars->kfull[gj & 7];
+                    if (lane == 0) mbar_arrive_expect_tx(full, C::TILE);
                     __syncwarp();
                     if (half < C::HALVES)
                         tma_load_4d(ring + s * C::TILE + half * C::HALF + mine * box_rows * 128,
-                                    kv ? &tmV : &tmK, &bars->full[s], half * 64, y, it.hk, z);
+                                    kv ? &tmV : &tmK, full, half * 64, y, it.hk, z);
+                    ++fills;
                 }
                 if (!ok) break;
             }
         }
         if (!ok)  // a wait gave up: the copies in flight land before the CTA's memory goes
-            for (int n = max(0, 2 * gj + 1 - C::NS); n < 2 * gj + 2; ++n)
-                (void)mbar_wait(&bars->full[n % C::NS], (n / C::NS) & 1);
-    } else if (warp == W_MMA) {
-        // ------------------------------ MMA issuer --------------------------------------
+            for (int n = max(0, fills - C::NS); n < fills; ++n)
+                (void)mbar_wait(n & 1 ? &bars->vfull[(n >> 1) & 7] : &bars->kfull[(n >> 1) & 7], (n >> 4) & 1);
+    } else if (warp == W_S) {
+        // ------------------------------ issuer of S -------------------------------------
         if (lane == 0) {
-            constexpr uint32_t kIdescS = idesc_f16(BF16, false, false, 128, 128);
-            constexpr uint32_t kIdescO = idesc_f16(BF16, false, true, 128, D);
+            constexpr uint32_t kIdesc = idesc_f16(BF16, false, false, 128, C::STEP);
             const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
             const uint64_t k_desc = smem_desc_sw128(smem_u32(ring), 16, 1024);
-            const uint64_t v_desc = smem_desc_sw128(smem_u32(ring), C::HALF, 1024);
-            int asked = 0;
-            // S of tile g (key tile j), row tile i (K's slot is released by the last row tile's)
-            auto issue_s = [&](int g, int i, int j) -> bool {
-                const int n = 2 * g, s = n % C::NS;
-                if (!mbar_wait(&bars->full[s], (n / C::NS) & 1)) return false;
-                if (g >= BUFS && !mbar_wait(&bars->s_empty[bi(g, i)], ph(g - BUFS))) return false;
-                tc_fence_after();
-                const uint64_t kd = k_desc + (uint64_t)((s * C::TILE) >> 4);
-                const uint64_t qd = q_desc + (uint64_t)((i * C::QTILE) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint64_t qo = (uint64_t)(((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4);
-                    const uint64_t ko = (uint64_t)(((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4);
-                    mma_ss(tmem + C::COL_S + bi(g, i) * 128, qd + qo, kd + ko, kIdescS, kk > 0);
-                }
-                if (i == RT - 1) mma_commit(&bars->empty[s]);
-                mma_commit(&bars->s_full[bi(g, i)]);
-                if (i == 0 && it.repair(p, j)) mbar_arrive(&bars->need[asked++ & 1]);
-                return true;
-            };
-            // P V of tile g, row tile i
-            auto issue_pv = [&](int g, int i, int s, bool first) {
-                tc_fence_after();
-                const uint64_t vd = v_desc + (uint64_t)((s * C::TILE) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ts(tmem + C::COL_O + i * D, tmem + C::COL_P + bi(g, i) * C::P_STEP + kk * 8,
-                           vd + (uint64_t)((kk * 16 * 128) >> 4), kIdescO, !first || kk > 0);
-                if (i == RT - 1) mma_commit(&bars->empty[s]);
-                mma_commit(&bars->pv_done[bi(g, i)]);
-            };
             bool ok = true;
-            int gj = 0, t = 0;
-            uint32_t fixes = 0;  // parity of each slot's next repair
+            int n0 = 0, t = 0;  // steps and pieces so far
+            int asked = 0;
             while (ok && paged_take(bars, np++, lane, false, it)) {
-                const int nt = it.j1 - it.j0;
-                if (nt <= 0) continue;
+                const int steps = (it.j1 - it.j0) * SPT;
+                if (steps <= 0) continue;
                 if (!mbar_wait(&bars->q_full, t & 1)) break;
-                tc_fence_after();
-                for (int i = 0; ok && i < RT; ++i) ok = issue_s(gj, i, it.j0);
-                for (int x = 0; ok && x < nt; ++x) {
-                    const int g = gj + x;
-                    const int n = 2 * g + 1, s = n % C::NS;
-                    const bool more = x + 1 < nt;
+                for (int x = 0; ok && x < steps; ++x) {
+                    const int n = n0 + x, h = x % SPT;
+                    const int g = n / SPT, s = 2 * g % C::NS;  // tile, K's slot
+                    if (h == 0 && !mbar_wait(&bars->kfull[g & 7], (g >> 3) & 1)) { ok = false; break; }
+                    const uint64_t kd = k_desc + (uint64_t)((s * C::TILE + h * C::STEP * 128) >> 4);
 #pragma unroll
                     for (int i = 0; i < RT; ++i) {
-                        // the next tile's S first where its buffer is another one or is read
-                        // before P is written; behind P V where P overwrites S
-                        if (C::P_OWN && more && !issue_s(g + 1, i, it.j0 + x + 1)) { ok = false; break; }
-                        if (!more && i == RT - 1 && C::P_OWN) mma_commit(&bars->q_empty);
-                        if (!mbar_wait(&bars->p_full[bi(g, i)], ph(g))) { ok = false; break; }
-                        if (i == 0) {
-                            if (!mbar_wait(&bars->full[s], (n / C::NS) & 1)) { ok = false; break; }
-                            if (it.repair(p, it.j0 + x)) {
-                                if (!mbar_wait(&bars->fixed[s], (fixes >> s) & 1)) { ok = false; break; }
-                                fixes ^= 1u << s;
-                            }
-                            if (x == 0 && t > 0 && !mbar_wait(&bars->o_empty, (t - 1) & 1)) {
-                                ok = false;
-                                break;
-                            }
+                        // the buffer held the scores (P_OWN) or the weights of step n - 2
+                        const int b = bi(n, i);
+                        if (n >= 2 && !mbar_wait(C::P_OWN ? &bars->s_empty[b] : &bars->pv_done[b], ph(n - 2))) {
+                            ok = false;
+                            break;
                         }
-                        issue_pv(g, i, s, x == 0);
-                        if (!C::P_OWN && more && !issue_s(g + 1, i, it.j0 + x + 1)) { ok = false; break; }
-                        if (!more && i == RT - 1 && !C::P_OWN) mma_commit(&bars->q_empty);
+                        tc_fence_after();
+                        const uint64_t qd = q_desc + (uint64_t)((i * C::QTILE) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t qo = (uint64_t)(((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4);
+                            const uint64_t ko = (uint64_t)(((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4);
+                            mma_ss(tmem + C::COL_S + b * C::STEP, qd + qo, kd + ko, kIdesc, kk > 0);
+                        }
+                        // (the barriers that nobody waits for at the end come first, so that no
+                        // arrival is outstanding when the CTA ends)
+                        if (i == RT - 1 && h == SPT - 1) mma_commit(&bars->empty[s]);
+                        if (i == RT - 1 && x == steps - 1) mma_commit(&bars->q_empty);
+                        mma_commit(&bars->s_full[b]);
+                    }
+                    if (!ok) break;
+                    if (h == 0 && it.repair(p, it.j0 + x / SPT)) mbar_arrive(&bars->need[asked++ & 3]);
+                }
+                n0 += steps;
+                ++t;
+            }
+        }
+    } else if (warp == W_PV) {
+        // ------------------------------ issuer of P V -----------------------------------
+        if (lane == 0) {
+            constexpr uint32_t kIdesc = idesc_f16(BF16, false, true, 128, D);
+            const uint64_t v_desc = smem_desc_sw128(smem_u32(ring), C::HALF, 1024);
+            bool ok = true;
+            int n0 = 0, t = 0;
+            uint32_t fixes = 0;  // parity of the next repair of each of the eight
+            while (ok && paged_take(bars, np++, lane, false, it)) {
+                const int steps = (it.j1 - it.j0) * SPT;
+                if (steps <= 0) continue;
+                for (int x = 0; ok && x < steps; ++x) {
+                    const int n = n0 + x, h = x % SPT;
+                    const int g = n / SPT, s = (2 * g + 1) % C::NS;  // tile, V's slot
+                    if (h == 0) {
+                        if (!mbar_wait(&bars->vfull[g & 7], (g >> 3) & 1)) { ok = false; break; }
+                        if (it.repair(p, it.j0 + x / SPT)) {
+                            if (!mbar_wait(&bars->fixed[g & 7], (fixes >> (g & 7)) & 1)) { ok = false; break; }
+                            fixes ^= 1u << (g & 7);
+                        }
+                        if (x == 0 && t > 0 && !mbar_wait(&bars->o_empty, (t - 1) & 1)) { ok = false; break; }
+                    }
+                    const uint64_t vd = v_desc + (uint64_t)((s * C::TILE + h * C::STEP * 128) >> 4);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        const int b = bi(n, i);
+                        if (!mbar_wait(&bars->p_full[b], ph(n))) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t pa = tmem + (C::P_OWN ? C::COL_P + (n & 1) * C::P_STEP
+                                                             : C::COL_S + b * C::STEP);
+#pragma unroll
+                        for (int kk = 0; kk < C::STEP / 16; ++kk)
+                            mma_ts(tmem + C::COL_O + i * D, pa + kk * 8,
+                                   vd + (uint64_t)((kk * 16 * 128) >> 4), kIdesc, x > 0 || kk > 0);
+                        if (i == RT - 1 && h == SPT - 1) mma_commit(&bars->empty[s]);
+                        mma_commit(&bars->pv_done[b]);
                     }
                 }
-                gj += nt;
+                n0 += steps;
                 ++t;
             }
         }
     } else if (warp == W_FIX) {
-        // ------------------------------ Q loads, V repairs ------------------------------
-        bool ok = true;
+        // ------------------------------ pieces, Q loads, V repairs ----------------------
+        PagedWalk<RT> walk;
+        walk.init(p, lane);
+        bool ok = walk.step(p, bars, lane) && walk.step(p, bars, lane);
+        if (blockIdx.x == 0)
+            for (int b = lane; b < p.B; b += 32) page_lengths_check(p.pt, p.T, b);
         int gj = 0, t = 0, served = 0;
         while (ok && paged_take(bars, np++, lane, true, it)) {
+            if (!(ok = walk.step(p, bars, lane))) break;
             const int nt = it.j1 - it.j0;
             if (nt <= 0) continue;
             if (t > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (t - 1) & 1))) break;
@@ -557,9 +602,9 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             for (int i = 0; ok && i < nt; ++i) {
                 const int j = it.j0 + i;
                 if (!it.repair(p, j)) continue;
-                const int n = 2 * (gj + i) + 1, s = n % C::NS;
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars->need[served & 1], (served >> 1) & 1) &&
-                                                 mbar_wait(&bars->full[s], (n / C::NS) & 1));
+                const int g = gj + i, s = (2 * g + 1) % C::NS;
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->need[served & 3], (served >> 2) & 1) &&
+                                                 mbar_wait(&bars->vfull[g & 7], (g >> 3) & 1));
                 if (!ok) break;
                 ++served;
                 // (the swizzle permutes 16-byte chunks within a row only)
@@ -591,14 +636,14 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 if (lane == 0) bars->poison[t & 3] = found ? 1 : 0;
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->fixed[s]);
+                if (lane == 0) mbar_arrive(&bars->fixed[g & 7]);
             }
             ++t;
             gj += nt;
         }
         // the last Q load has landed before the CTA's memory goes (at once unless a wait gave up)
         if (t > 0) (void)mbar_wait(&bars->q_full, (t - 1) & 1);
-    } else if (warp < C::SOFT) {
+    } else {
         // ------------------------------ softmax warps -----------------------------------
         constexpr int WPC = 4 / REP;                       // warps of one copy of the rows
         const int ti = RT == 1 ? 0 : warp >> 2;            // row tile
@@ -617,7 +662,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             for (int i = 0; i < 4; ++i) tmem_st32(tmem + lane_base + C::COL_P + i * 32, zero);
         }
         bool ok = true;
-        int gj = 0, t = 0;
+        int n0 = 0, t = 0;  // steps and pieces so far
         while (paged_take(bars, np++, lane, true, it)) {
             const int tok = it.tok0 + ti * p.TPT + tl;
             const int head = it.g0 + gl;                   // among the key/value head's
@@ -627,11 +672,11 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             float m = -INFINITY;   // running maximum, base 2
             float l = 0.f;         // running sum
             float lr = 0.f;        // the same sum of the rounded weights
-            for (int i = 0; ok && i < nt; ++i) {
-                const int g = gj + i;
-                const int b = bi(g, ti);
-                const int k0 = (it.j0 + i) * 128 + kw * CW;  // first key of this thread
-                const uint32_t sb = tmem + lane_base + C::COL_S + b * 128 + kw * CW;
+            for (int i = 0; ok && i < nt * SPT; ++i) {
+                const int n = n0 + i, b = bi(n, ti);
+                const int kt = i % SPT * C::STEP + kw * CW;        // this thread's keys of the tile
+                const int k0 = (it.j0 + i / SPT) * 128 + kt;
+                const uint32_t sb = tmem + lane_base + C::COL_S + b * C::STEP + kw * CW;
                 // Keys from the first new one on: the row's visible ones (held keys all are).
                 bool masked = k0 + CW > it.past;
                 if (masked) {
@@ -657,12 +702,12 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         bars->vis[w][threadIdx.x] = bits;
                     }
                 }
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[b], ph(g)))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[b], ph(n)))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t bad = bars->bad[g & 15];
+                const uint32_t bad = bars->bad[(n / SPT) & 15];
                 // First pass over the scores: the maximum.  (The passes read the scores from
                 // TMEM 32 or 64 at a time in loops: unrolled over a row's 128 the code took
                 // 4 us to come in from memory at a kernel's first tile, against 1.1 us a tile
@@ -676,10 +721,10 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     for (int w = 0; w < CW / 32; ++w) {
                         uint32_t bits = masked ? bars->vis[w][threadIdx.x] : 0xffffffffu;
                         if (bad) {  // keys of pages outside the cache are not visible
-                            const int sh = min(p.pt.page_shift, 7), n = min(1 << sh, 32);
-                            for (int c = 0; c < 32; c += n)
-                                if ((bad >> ((kw * CW + w * 32 + c) >> sh)) & 1u)
-                                    bits &= ~((n == 32 ? 0xffffffffu : (1u << n) - 1u) << c);
+                            const int sh = min(p.pt.page_shift, 7), sub = min(1 << sh, 32);
+                            for (int c = 0; c < 32; c += sub)
+                                if ((bad >> ((kt + w * 32 + c) >> sh)) & 1u)
+                                    bits &= ~((sub == 32 ? 0xffffffffu : (1u << sub) - 1u) << c);
                         }
                         uint32_t rr[32];
                         tmem_ld32(sb + w * 32, rr);
@@ -715,15 +760,16 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     m = mx;
                 }
                 const float m_use = (m == -INFINITY) ? 0.f : m;
-                // P's buffer is free once the last P V that read it is done (where P overwrites
-                // S it is); O may be rescaled once the previous tile's P V is.
-                if (g >= BUFS &&
-                    !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[b], ph(g - BUFS)))) {
+                // P's buffer is free once P V of step n - 2 is done (where P overwrites S it
+                // is: the wait keeps the phases in order); O may be rescaled once that of step
+                // n - 1 is.
+                if (n >= 2 &&
+                    !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[b], ph(n - 2)))) {
                     ok = false;
                     break;
                 }
                 if (i > 0 && any_grow) {
-                    if (RT == 1 && !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[bi(g - 1, ti)], ph(g - 1)))) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[bi(n - 1, ti)], ph(n - 1)))) {
                         ok = false;
                         break;
                     }
@@ -741,7 +787,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 // Second pass: the weights, their sums, P.  (P overwrites S behind the reads.)
                 float2 ls = make_float2(0.f, 0.f), rs = make_float2(0.f, 0.f);
                 const float2 sc = make_float2(sl2, sl2), nm = make_float2(-m_use, -m_use);
-                const uint32_t pb = tmem + lane_base + C::COL_P + b * C::P_STEP + kw * (CW / 2);
+                const uint32_t pb = C::P_OWN ? tmem + lane_base + C::COL_P + (n & 1) * C::P_STEP + kw * (CW / 2) : sb;
                 auto weights = [&](const uint32_t (&rr)[32], uint32_t dst) {
                     uint32_t pk[16];
 #pragma unroll
@@ -777,14 +823,14 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 l = l * alpha + (ls.x + ls.y);
                 lr = lr * alpha + (rs.x + rs.y);
                 tc_fence_before();
-                mbar_arrive(&bars->s_empty[b]);
+                if (C::P_OWN) mbar_arrive(&bars->s_empty[b]);
                 mbar_arrive(&bars->p_full[b]);
             }
 
             // ------------------------------ epilogue of the piece ------------------------
             if (ok && nt > 0) {
-                const int g = gj + nt - 1;
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[bi(g, ti)], ph(g)));
+                const int n = n0 + nt * SPT - 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[bi(n, ti)], ph(n)));
                 tc_fence_after();
             }
             // (the merge of the copies has barriers of all four warps: they leave together)
@@ -834,21 +880,35 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         tc_fence_before();
                         mbar_arrive(&bars->o_empty);
                     }
-                    if (!mine) continue;
                     if (poison && live) add_not_finite(v, 32, c32 * 32, tok);
                     if (it.whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(out_row(head, tok)) + c32 * 4;
+                        // through shared memory, so that a store covers 64 bytes of 8 rows
+                        // instead of 16 bytes of 32 (16-byte chunks permuted by row pairs)
+                        uint4 *st = reinterpret_cast<uint4 *>(smem + C::OFF_MERGE + warp * 2048);
+                        __syncwarp();
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            dst[e] = make_uint4(pack2<BF16>(v[8 * e], v[8 * e + 1]),
-                                                pack2<BF16>(v[8 * e + 2], v[8 * e + 3]),
-                                                pack2<BF16>(v[8 * e + 4], v[8 * e + 5]),
-                                                pack2<BF16>(v[8 * e + 6], v[8 * e + 7]));
+                            st[lane * 4 + (e ^ ((lane >> 1) & 3))] =
+                                make_uint4(pack2<BF16>(v[8 * e], v[8 * e + 1]),
+                                           pack2<BF16>(v[8 * e + 2], v[8 * e + 3]),
+                                           pack2<BF16>(v[8 * e + 4], v[8 * e + 5]),
+                                           pack2<BF16>(v[8 * e + 6], v[8 * e + 7]));
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int rl = e * 8 + (lane >> 2), r = (wq << 5) + rl, q = lane & 3;
+                            const int tr = r * p.gp_magic >> 16, hr = r - tr * p.GP + it.g0;
+                            const int tk = it.tok0 + ti * p.TPT + tr;
+                            if (tr < p.TPT && tk < p.T && hr < p.G)
+                                reinterpret_cast<uint4 *>(out_row(hr, tk))[c32 * 4 + q] =
+                                    st[rl * 4 + (q ^ ((rl >> 1) & 3))];
+                        }
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + (prow0 + row) * D) + c32 * 8;
+                        // a piece: [column / 4][row] of four columns, whole lines at a time
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow0 * D) + c32 * 8 * ROWS + row;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                            dst[e * ROWS] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     }
                 }
             } else {
@@ -858,11 +918,24 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 // used rows are few, else 32 at a time.  O = sum_k (f_k / R) O_k.
                 float *buf = reinterpret_cast<float *>(smem + C::OFF_MERGE);
                 const int used = min(p.TPT, p.T) * p.GP;
-                const bool once = REP * used * (D + 4) * 4 <= C::MERGE;
+                constexpr int MAXR = 4;                        // rows of a thread at most
+                const bool once = REP * used * (D + 4) * 4 <= C::MERGE && used <= MAXR * (512 / D);
                 const int pitch = (once ? D : 32) + 4;
                 const int qs = once ? (D == 64 ? 4 : 5) : 3;   // log2 of 4-column groups
                 const int x = wq * 32 + lane;
                 const int c4 = (x & ((1 << qs) - 1)) * 4;      // this thread's columns
+                void *dst[MAXR];                               // of its rows, at column c4
+                int dtok[MAXR];
+#pragma unroll
+                for (int e = 0; e < MAXR; ++e) {
+                    const int r = (x >> qs) + e * (128 >> qs);
+                    const int rl = r * p.gp_magic >> 16, h = it.g0 + (r - rl * p.GP);
+                    dtok[e] = it.tok0 + rl;
+                    dst[e] = nullptr;
+                    if (r < used && dtok[e] < p.T && h < p.G)
+                        dst[e] = it.whole ? (void *)(out_row(h, dtok[e]) + c4)
+                                          : (void *)(p.part_o + (prow0 + r) * D + c4);
+                }
                 float scale = 0.f;
                 if (nt > 0) {
                     bars->stat[0][x] = m;
@@ -908,27 +981,27 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         }
                         named_bar_sync(1, 128);
                     }
-#pragma unroll 2
-                    for (int r = x >> qs; r < used; r += 128 >> qs) {
+#pragma unroll
+                    for (int e = 0; e < MAXR; ++e) {
+                        if (dst[e] == nullptr) continue;
+                        const float *src = buf + ((x >> qs) + e * (128 >> qs)) * pitch + c4;
                         float v[4] = {0.f, 0.f, 0.f, 0.f};
                         if (nt > 0) {
 #pragma unroll
                             for (int k = 0; k < REP; ++k) {
-                                const float4 y = *reinterpret_cast<const float4 *>(buf + (k * used + r) * pitch + c4);
+                                const float4 y = *reinterpret_cast<const float4 *>(src + k * used * pitch);
                                 v[0] += y.x;
                                 v[1] += y.y;
                                 v[2] += y.z;
                                 v[3] += y.w;
                             }
                         }
-                        const int rl = r * p.gp_magic >> 16, tk = it.tok0 + rl, h = it.g0 + (r - rl * p.GP);
-                        if (tk >= p.T || h >= p.G) continue;
-                        if (poison && tk < it.fresh) add_not_finite(v, 4, c0 + c4, tk);
+                        if (poison && dtok[e] < it.fresh) add_not_finite(v, 4, c0 + c4, dtok[e]);
                         if (it.whole)
-                            *reinterpret_cast<uint2 *>(out_row(h, tk) + c0 + c4) =
+                            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst[e]) + c0) =
                                 make_uint2(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]));
                         else
-                            *reinterpret_cast<float4 *>(p.part_o + (prow0 + r) * D + c0 + c4) =
+                            *reinterpret_cast<float4 *>(static_cast<float *>(dst[e]) + c0) =
                                 make_float4(v[0], v[1], v[2], v[3]);
                     }
                 }
@@ -940,14 +1013,9 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 else
                     p.part_lse[prow0 + row] = lse2;
             }
-            gj += nt;
+            n0 += nt * SPT;
             if (nt > 0) ++t;
         }
-    } else {
-        // ------------------------------ pieces of work ----------------------------------
-        if (blockIdx.x == 0)
-            for (int b = lane; b < p.B; b += 32) page_lengths_check(p.pt, p.T, b);
-        paged_walk<RT>(p, bars, lane);
     }
 
     tc_fence_before();
@@ -958,74 +1026,109 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 
 // Merges the pieces of the items that were cut: with the pieces' log-sum-exps L_s (base 2),
 //   LSE = M + log2 sum_s 2^(L_s - M), O = sum_s 2^(L_s - LSE) O_s.
-// One warp per row; grid = (items, groups of 4 rows).  `rows`: of a row tile.
-template <int D, bool BF16, int RT>
-__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_constant__ PagedParams p,
+// The pieces and their places are worked out before the wait for the attention kernel (which
+// triggers this launch behind its own wait, so that the lengths are final by then).
+// TRANS (rows of a piece as [column / 4][row]): grid = (items, groups of 32 rows), a lane is
+// a row, a warp 1 / 8 of the columns.  Else: grid = (items, groups of 16 rows), a warp is a
+// row at a time, a lane 1 / 32 of the columns.
+template <int D, bool BF16, int RT, bool TRANS>
+__global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_constant__ PagedParams p,
                                                              const int rows) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int item = blockIdx.x;
     const int rt = item % p.row_tiles, hk = (item / p.row_tiles) % p.Hk, b = item / p.row_tiles / p.Hk;
-    const int row = blockIdx.y * 4 + warp;             // of the item
-    const int tile = row / rows, r = row - tile * rows;
-    const int tl = r * p.gp_magic >> 16, tt = rt / p.GT;
-    const int tok = (tt * RT + tile) * p.TPT + tl, head = (rt - tt * p.GT) * p.GP + (r - tl * p.GP);
+    const PagedSeq s = paged_seq<RT>(p, b);
+    bool cut = rt < s.valid;
+    int c0 = 0, c1 = 0, first = 0;
+    if (cut) {
+        int W = 0, base = 0;  // all units, those before the sequence
+        for (int k = lane; k < p.B; k += 32) {
+            const int n = paged_seq<RT>(p, k).per_head * p.Hk;
+            W += n;
+            base += k < b ? n : 0;
+        }
+        W = warp_sum(W);
+        base = warp_sum(base);
+        PagedShares sh;
+        sh.init(W, p.ctas);
+        const int u0 = base + hk * s.per_head + rt * (s.tiles + kItemCost);
+        c0 = sh.of(u0);
+        c1 = sh.of(u0 + s.tiles - 1);
+        cut = c0 != c1;
+        // the first piece lies in CTA c0's second slot if that share began before the item
+        first = sh.begin(c0) < u0 ? 1 : 0;
+    }
     pdl_wait();
     pdl_launch_dependents();
-    if (row >= RT * rows || tl >= p.TPT || tok >= p.T || head >= p.G) return;
-    const PagedSeq s = paged_seq<RT>(p, b);
-    if (rt >= s.valid) return;
-    int W = 0, base = 0;  // all units, those before the sequence
-    for (int k = lane; k < p.B; k += 32) {
-        const int n = paged_seq<RT>(p, k).per_head * p.Hk;
-        W += n;
-        base += k < b ? n : 0;
-    }
-    W = warp_sum(W);
-    base = warp_sum(base);
-    PagedShares sh;
-    sh.init(W, p.ctas);
-    const int u0 = base + hk * s.per_head + rt * (s.tiles + kItemCost);
-    const int c0 = sh.of(u0), c1 = sh.of(u0 + s.tiles - 1);
-    if (c0 == c1) return;
-    // the first piece lies in CTA c0's second slot if that share began before the item
-    const int first = sh.begin(c0) < u0 ? 1 : 0;
-    auto at = [&](int c) -> long long { return (2LL * c + (c == c0 ? first : 0)) * (RT * rows) + row; };
-    float M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_lse[at(c)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    constexpr int E = D / 32;  // columns of a lane
-    float acc[E], sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-        const float ls = p.part_lse[at(c)];
-        const float w = ls == -INFINITY ? 0.f : ex2(ls - M);
-        const float *src = p.part_o + at(c) * D + lane * E;
-        float v[E];
-        if constexpr (E == 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(src);
-            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    if (!cut) return;
+    constexpr int NR = TRANS ? 1 : 2;  // rows of a thread
+#pragma unroll 1
+    for (int k = 0; k < NR; ++k) {
+        const int row = TRANS ? blockIdx.y * 32 + lane : blockIdx.y * 16 + k * 8 + warp;  // of the item
+        const int tile = row / rows, r = row - tile * rows;
+        const int tl = r * p.gp_magic >> 16, tt = rt / p.GT;
+        const int tok = (tt * RT + tile) * p.TPT + tl, head = (rt - tt * p.GT) * p.GP + (r - tl * p.GP);
+        if (tile >= RT || tl >= p.TPT || tok >= p.T || head >= p.G) continue;
+        auto at = [&](int c) -> long long { return (2LL * c + (c == c0 ? first : 0)) * (RT * rows); };
+        float M = -INFINITY;
+        if constexpr (TRANS) {
+#pragma unroll 8
+            for (int c = c0; c <= c1; ++c) M = fmaxf(M, p.part_lse[at(c) + row]);
         } else {
-            const float2 x = *reinterpret_cast<const float2 *>(src);
-            v[0] = x.x; v[1] = x.y;
-        }
-        sum += w;
+            for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_lse[at(c) + row]);
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        }
+        constexpr int E = TRANS ? D / 8 : D / 32;  // columns of a thread
+        float acc[E], sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll TRANS ? 2 : 8
+        for (int c = c0; c <= c1; ++c) {
+            const float ls = p.part_lse[at(c) + row];
+            const float w = ls == -INFINITY ? 0.f : ex2(ls - M);
+            sum += w;
+            if constexpr (TRANS) {
+                const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (at(c) + tile * rows) * D) +
+                                    warp * (E / 4) * rows + r;
+#pragma unroll
+                for (int e = 0; e < E / 4; ++e) {
+                    const float4 x = src[e * rows];
+                    acc[4 * e] = fmaf(w, x.x, acc[4 * e]);
+                    acc[4 * e + 1] = fmaf(w, x.y, acc[4 * e + 1]);
+                    acc[4 * e + 2] = fmaf(w, x.z, acc[4 * e + 2]);
+                    acc[4 * e + 3] = fmaf(w, x.w, acc[4 * e + 3]);
+                }
+            } else {
+                const float2 *src = reinterpret_cast<const float2 *>(p.part_o + (at(c) + row) * D + lane * E);
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    const float2 x = src[e];
+                    acc[2 * e] = fmaf(w, x.x, acc[2 * e]);
+                    acc[2 * e + 1] = fmaf(w, x.y, acc[2 * e + 1]);
+                }
+            }
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int h = hk * p.G + head;
+        uint32_t *o = reinterpret_cast<uint32_t *>(const_cast<uint16_t *>(p.o.p) + b * p.o.sb + h * p.o.sh +
+                                                   tok * p.o.st + (TRANS ? warp : lane) * E);
+        uint32_t w[E / 2];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) w[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        if constexpr (E / 2 >= 4) {
+#pragma unroll
+            for (int e = 0; e < E / 8; ++e)
+                reinterpret_cast<uint4 *>(o)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        } else if constexpr (E / 2 == 2) {
+            *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+        } else {
+            *o = w[0];
+        }
+        if (TRANS ? warp == 0 : lane == 0)
+            p.lse[((long long)b * p.Hk * p.G + h) * p.T + tok] =
+                sum == 0.f ? -INFINITY : (M + lg2(sum)) * 0.69314718055994531f;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int h = hk * p.G + head;
-    uint16_t *o = const_cast<uint16_t *>(p.o.p) + b * p.o.sb + h * p.o.sh + tok * p.o.st + lane * E;
-    if constexpr (E == 4)
-        *reinterpret_cast<uint2 *>(o) = make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv),
-                                                   pack2<BF16>(acc[2] * inv, acc[3] * inv));
-    else
-        *reinterpret_cast<uint32_t *>(o) = pack2<BF16>(acc[0] * inv, acc[1] * inv);
-    if (lane == 0)
-        p.lse[((long long)b * p.Hk * p.G + h) * p.T + tok] =
-            sum == 0.f ? -INFINITY : (M + lg2(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace fa

@@ -105,6 +105,8 @@ LONG = [
     (4, 8, 8, 13, 64, 64, [4000, 6100, 77, 2049], FP, None, False),
     (4, 8, 8, 20, 128, 16, [3500, 6000, 1, 4444], BF, [20, 17, 20, 4], True),
     (3, 8, 4, 70, 64, 128, [7000, 2500, 4100], BF, None, False),
+    (8, 4, 4, 1, 128, 64, [16000] * 8, BF, None, False),   # tiles come in slower than they are used
+    (8, 4, 4, 1, 64, 64, [20000] * 8, FP, None, False),
     (600, 4, 3, 1, 64, 16, [(97 * i) % 520 for i in range(600)], FP, None, False),
 ]
 
