@@ -77,20 +77,23 @@ struct PagedCfg {
     static constexpr int OFF_RING = OFF_Q + RT * QTILE;
     static constexpr int OFF_MERGE = OFF_RING + NS * TILE;
     static constexpr int OFF_BAR = OFF_MERGE + MERGE;
-    static constexpr int USED = OFF_BAR + 2816 + 4096;
+    static constexpr int USED = OFF_BAR + 3072 + 8192;
     static constexpr int SMEM = USED + 1024;
     static constexpr int SOFT = 4 * RT;         // softmax warps
     static constexpr int THREADS = 32 * (SOFT + 4);
-    // The softmax goes in steps of a whole tile (RT = 1) or 64 keys (RT = 2).  TMEM: two
-    // score buffers per row tile in turn, so that a step's S is there before the last step's
-    // P V is; P has columns of its own (RT = 1) or overwrites S.
+    // The softmax goes in steps: whole tiles (RT = 1) or 64 keys (RT = 2), whose scores a
+    // thread holds in registers, so that the one score buffer that TMEM has room for at
+    // d = 128 is free for the next step's S at once.  (A chunk of 512 tokens against 16K keys,
+    // d = 128: 103 us in steps of 128 with P over S, 93 us in steps of 64 with two buffers and
+    // P over S; see the kernel for this form's.)
     static constexpr int SPT = RT;              // steps of a tile
     static constexpr int STEP = BN / SPT;       // keys of a step
-    static constexpr bool P_OWN = RT == 1;
-    static constexpr uint32_t COL_S = 0;
-    static constexpr uint32_t COL_P = P_OWN ? 256 : 0;
-    static constexpr uint32_t P_STEP = 64;      // between the two buffers of P
-    static constexpr uint32_t COL_O = P_OWN ? 384 : 256;
+    static constexpr int NSB = (RT == 1) ? 2 : 1;  // score buffers of a row tile
+    // TMEM columns: scores, two buffers of P, O
+    static constexpr uint32_t S_TILE = (RT == 1) ? 0 : 128;  // between row tiles
+    static constexpr uint32_t COL_P = (RT == 1) ? 256 : 64;
+    static constexpr uint32_t P_BUF = STEP / 2;
+    static constexpr uint32_t COL_O = (RT == 1) ? 384 : 256;
     static_assert(COL_O + RT * D <= 512, "TMEM budget");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -102,14 +105,15 @@ struct PagedBars {
     // warp waits for is unambiguous.  (Four in turn: S runs at most four tiles ahead of a
     // repair, as P V of the first waits for it.)
     uint64_t need[4];
-    // index: 2 * row tile + the step's parity
-    uint64_t s_full[4], s_empty[4], p_full[4], pv_done[4];
+    uint64_t s_full[2], s_empty[2];   // index: score buffer (RT = 1) or row tile
+    uint64_t p_full[4], pv_done[4];   // index: 2 * row tile + buffer of P
     // Fills are announced per tile (mod 8; a ring holds at most 6), K and V apart, so that
     // each is waited for in order by the issuer that uses it; a ring slot, which K and V may
     // take in turn, is released per slot.  fixed: V repaired.
     uint64_t kfull[8], vfull[8], fixed[8];
     uint64_t empty[12];
     uint64_t seg_full[4], seg_empty[4];
+    uint64_t mask_full[2], mask_empty[2];
     uint32_t tmem_base;
     int4 seg[4][3];         // ring of pieces (PagedSeg)
     uint32_t bad[16];       // per tile: sub-pages whose page number is outside the cache
@@ -117,7 +121,7 @@ struct PagedBars {
     // t + 4 only after the softmax of item t + 1 began.)
     int poison[4];
     float stat[3][128];     // REP merge: m, l, l of the rounded weights
-    uint32_t vis[4][256];   // per softmax thread: keys of the tile that its row sees
+    uint32_t mask[2][1024]; // per token of the piece, up to 128 bits: the new keys it sees
 };
 
 // Work units of a sequence: for each of its items with a new token the key tiles and kItemCost
@@ -176,15 +180,16 @@ struct PagedSeg {
     int j0, j1;
     int slot;           // of the workspace, if the item was cut
     int whole;
-    // Whether some row may see fewer new keys than another.
-    __device__ __forceinline__ bool hides(const PagedParams &p) const {
-        return fresh > 1 || p.tree != nullptr;
+    // Keys that every new token from `tok` on sees: the held ones, and in a chain the new
+    // ones up to `tok`.
+    __device__ __forceinline__ int open(const PagedParams &p, int tok) const {
+        return p.tree ? past : min(past + tok + 1, total);
     }
-    // Whether warp 6 goes over V tile j: slots behind the last key, whose contents are
+    // Whether V tile j is gone over: slots behind the last key, whose contents are
     // unspecified, are cleared (0 * NaN would reach O), and so are values that are not
-    // finite in keys that some row may not see.
+    // finite in keys that some row does not see.
     __device__ __forceinline__ bool repair(const PagedParams &p, int j) const {
-        return (j + 1) * 128 > (hides(p) ? past : total);
+        return (j + 1) * 128 > open(p, tok0);
     }
 };
 
@@ -386,13 +391,16 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint8_t *sQ = smem + C::OFF_Q;
     uint8_t *ring = smem + C::OFF_RING;
     PagedBars *bars = reinterpret_cast<PagedBars *>(smem + C::OFF_BAR);
-    static_assert(sizeof(PagedBars) <= 2816 + 4096, "barrier area");
+    static_assert(sizeof(PagedBars) <= 3072 + 8192, "barrier area");
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
-    // Barrier index and phase of step n, row tile i.
-    auto bi = [](int n, int i) { return 2 * i + (n & 1); };
-    auto ph = [](int n) { return (n >> 1) & 1; };
+    // Step n, row tile i: score buffer's barrier and phase, P buffer's barrier and phase.
+    constexpr int NSB = C::NSB;
+    auto sb_of = [](int n, int i) { return NSB == 2 ? (n & 1) : i; };
+    auto sb_ph = [](int n) { return NSB == 2 ? (n >> 1) & 1 : n & 1; };
+    auto pb_of = [](int n, int i) { return 2 * i + (n & 1); };
+    auto pb_ph = [](int n) { return (n >> 1) & 1; };
 
     if (threadIdx.x == W_S * 32) {
         tma_prefetch_desc(&tmQ);
@@ -402,9 +410,15 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         mbar_init(&bars->q_empty, 1);
         mbar_init(&bars->o_empty, 128 * RT);
         for (int i = 0; i < 4; ++i) mbar_init(&bars->need[i], 1);
-        for (int i = 0; i < 2 * RT; ++i) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->mask_full[i], 1);
+            mbar_init(&bars->mask_empty[i], C::SOFT);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->s_full[i], 1);
             mbar_init(&bars->s_empty[i], 128);
+        }
+        for (int i = 0; i < 2 * RT; ++i) {
             mbar_init(&bars->p_full[i], 128);
             mbar_init(&bars->pv_done[i], 1);
         }
@@ -503,9 +517,8 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     const uint64_t kd = k_desc + (uint64_t)((s * C::TILE + h * C::STEP * 128) >> 4);
 #pragma unroll
                     for (int i = 0; i < RT; ++i) {
-                        // the buffer held the scores (P_OWN) or the weights of step n - 2
-                        const int b = bi(n, i);
-                        if (n >= 2 && !mbar_wait(C::P_OWN ? &bars->s_empty[b] : &bars->pv_done[b], ph(n - 2))) {
+                        const int b = sb_of(n, i);
+                        if (n >= NSB && !mbar_wait(&bars->s_empty[b], sb_ph(n - NSB))) {
                             ok = false;
                             break;
                         }
@@ -515,7 +528,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint64_t qo = (uint64_t)(((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4);
                             const uint64_t ko = (uint64_t)(((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4);
-                            mma_ss(tmem + C::COL_S + b * C::STEP, qd + qo, kd + ko, kIdesc, kk > 0);
+                            mma_ss(tmem + b * 128, qd + qo, kd + ko, kIdesc, kk > 0);
                         }
                         // (the barriers that nobody waits for at the end come first, so that no
                         // arrival is outstanding when the CTA ends)
@@ -555,11 +568,10 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     const uint64_t vd = v_desc + (uint64_t)((s * C::TILE + h * C::STEP * 128) >> 4);
 #pragma unroll
                     for (int i = 0; i < RT; ++i) {
-                        const int b = bi(n, i);
-                        if (!mbar_wait(&bars->p_full[b], ph(n))) { ok = false; break; }
+                        const int b = pb_of(n, i);
+                        if (!mbar_wait(&bars->p_full[b], pb_ph(n))) { ok = false; break; }
                         tc_fence_after();
-                        const uint32_t pa = tmem + (C::P_OWN ? C::COL_P + (n & 1) * C::P_STEP
-                                                             : C::COL_S + b * C::STEP);
+                        const uint32_t pa = tmem + C::COL_P + i * C::S_TILE + (n & 1) * C::P_BUF;
 #pragma unroll
                         for (int kk = 0; kk < C::STEP / 16; ++kk)
                             mma_ts(tmem + C::COL_O + i * D, pa + kk * 8,
@@ -579,7 +591,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         bool ok = walk.step(p, bars, lane) && walk.step(p, bars, lane);
         if (blockIdx.x == 0)
             for (int b = lane; b < p.B; b += 32) page_lengths_check(p.pt, p.T, b);
-        int gj = 0, t = 0, served = 0;
+        int gj = 0, t = 0, served = 0, masks = 0;
         while (ok && paged_take(bars, np++, lane, true, it)) {
             if (!(ok = walk.step(p, bars, lane))) break;
             const int nt = it.j1 - it.j0;
@@ -597,7 +609,28 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                                     it.tok0 + (RT > 1 ? i * p.TPT : 0), it.b);
             }
             __syncwarp();
-            // V tiles with new keys or slots behind them
+            // The rows' masks as bits, one (token, 32 new keys) per lane at a time.
+            if (p.tree != nullptr && p.T <= 128 && it.j1 * 128 > it.past) {
+                uint32_t *mask = bars->mask[masks & 1];
+                if (masks >= 2 &&
+                    !(ok = __all_sync(0xffffffffu, mbar_wait(&bars->mask_empty[masks & 1], ((masks >> 1) - 1) & 1))))
+                    break;
+                const int nw = (it.fresh + 31) >> 5, toks = min(RT * p.TPT, it.fresh - it.tok0);
+                for (int k = lane; k < toks * nw; k += 32) {
+                    const int tk = k / nw, w = k - tk * nw;
+                    const uint8_t *mr = p.tree + it.b * p.tree_sb + (long long)(it.tok0 + tk) * p.T + w * 32;
+                    const int n = it.fresh - w * 32;
+                    uint32_t bits = 0u;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (c < n) bits |= (__ldg(mr + c) != 0 ? 1u : 0u) << c;
+                    mask[tk * 4 + w] = bits;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->mask_full[masks & 1]);
+                ++masks;
+            }
+            // V tiles with new keys that some row does not see, or slots behind the last
             bool found = false;
             for (int i = 0; ok && i < nt; ++i) {
                 const int j = it.j0 + i;
@@ -614,25 +647,33 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
                     for (int hf = 0; hf < C::HALVES; ++hf)
                         *reinterpret_cast<uint4 *>(tile + hf * C::HALF + x * 16) = make_uint4(0, 0, 0, 0);
-                if (it.hides(p)) {
-                    for (int x = max(0, it.past - j * 128) * 8 + lane; x < tail * 8; x += 32)
+                // (the exponent's all ones carry into the sign's place)
+                constexpr uint32_t kCarry = BF16 ? 0x00800080u : 0x04000400u;
+                const int x1 = tail * 8;
+                for (int x = max(0, it.open(p, it.tok0) - j * 128) * 8 + lane; x < x1; x += 128) {
+                    uint32_t hit = 0u;
 #pragma unroll
-                        for (int hf = 0; hf < C::HALVES; ++hf) {
-                            uint32_t *w = reinterpret_cast<uint32_t *>(tile + hf * C::HALF + x * 16);
-                            uint4 v = *reinterpret_cast<uint4 *>(w);
-                            const uint32_t hit = not_finite2<BF16>(v.x) | not_finite2<BF16>(v.y) |
-                                                 not_finite2<BF16>(v.z) | not_finite2<BF16>(v.w);
-                            if (hit) {
-                                found = true;
-                                v.x &= ~not_finite2<BF16>(v.x);
-                                v.y &= ~not_finite2<BF16>(v.y);
-                                v.z &= ~not_finite2<BF16>(v.z);
-                                v.w &= ~not_finite2<BF16>(v.w);
-                                *reinterpret_cast<uint4 *>(w) = v;
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int hf = 0; hf < C::HALVES; ++hf)
+                            if (x + e * 32 < x1) {
+                                const uint4 v = *reinterpret_cast<const uint4 *>(tile + hf * C::HALF + (x + e * 32) * 16);
+                                hit |= ((v.x & 0x7FFF7FFFu) + kCarry) | ((v.y & 0x7FFF7FFFu) + kCarry) |
+                                       ((v.z & 0x7FFF7FFFu) + kCarry) | ((v.w & 0x7FFF7FFFu) + kCarry);
                             }
+                    if (hit & 0x80008000u) {
+                        found = true;
+#pragma unroll 1
+                        for (int e = 0; e < 4 * C::HALVES; ++e) {
+                            const int xx = C::HALVES == 2 ? x + (e >> 1) * 32 : x + e * 32;
+                            if (xx >= x1) break;
+                            uint32_t *w = reinterpret_cast<uint32_t *>(tile + (C::HALVES == 2 ? (e & 1) * C::HALF : 0) + xx * 16);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) w[c] &= ~not_finite2<BF16>(w[c]);
                         }
-                    found = __any_sync(0xffffffffu, found);
+                    }
                 }
+                found = __any_sync(0xffffffffu, found);
                 if (lane == 0) bars->poison[t & 3] = found ? 1 : 0;
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -659,97 +700,104 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
             for (int i = 0; i < 32; ++i) zero[i] = 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_st32(tmem + lane_base + C::COL_P + i * 32, zero);
+            for (int i = 0; i < 2 * (int)C::P_BUF / 32; ++i) tmem_st32(tmem + lane_base + C::COL_P + i * 32, zero);
         }
         bool ok = true;
-        int n0 = 0, t = 0;  // steps and pieces so far
+        int n0 = 0, t = 0, masks = 0;  // steps, pieces and masks so far
         while (paged_take(bars, np++, lane, true, it)) {
             const int tok = it.tok0 + ti * p.TPT + tl;
             const int head = it.g0 + gl;                   // among the key/value head's
             const bool mine = tl < p.TPT && tok < p.T && head < p.G;  // a row of the call
             const bool live = mine && tok < it.fresh;      // a new token's row
             const int nt = max(it.j1 - it.j0, 0);
+            // (keys in front of it need no mask)
+            const int open = it.open(p, it.tok0 + ti * p.TPT);
+            // the piece's masks are in place (see the repairing warp)
+            const bool bits_used = p.tree != nullptr && p.T <= 128 && nt > 0 && it.j1 * 128 > it.past;
+            if (bits_used) ok = __all_sync(0xffffffffu, mbar_wait(&bars->mask_full[masks & 1], (masks >> 1) & 1));
             float m = -INFINITY;   // running maximum, base 2
             float l = 0.f;         // running sum
             float lr = 0.f;        // the same sum of the rounded weights
             for (int i = 0; ok && i < nt * SPT; ++i) {
-                const int n = n0 + i, b = bi(n, ti);
+                const int n = n0 + i, b = sb_of(n, ti);
                 const int kt = i % SPT * C::STEP + kw * CW;        // this thread's keys of the tile
                 const int k0 = (it.j0 + i / SPT) * 128 + kt;
-                const uint32_t sb = tmem + lane_base + C::COL_S + b * C::STEP + kw * CW;
-                // Keys from the first new one on: the row's visible ones (held keys all are).
-                bool masked = k0 + CW > it.past;
-                if (masked) {
-#pragma unroll 1
-                    for (int w = 0; w < CW / 32; ++w) {
-                        const int x0 = k0 + w * 32 - it.past;  // new key of bit 0
-                        uint32_t bits = 0u;
-                        if (live) {
-                            if (p.tree == nullptr) {
-                                const int n = tok + 1 - x0;    // keys up to the row's token
-                                bits = n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
-                            } else {
-                                bits = x0 >= 0 ? 0u : (x0 <= -32 ? 0xffffffffu : (1u << -x0) - 1u);
-                                const uint8_t *mr = p.tree + it.b * p.tree_sb + (long long)tok * p.T + x0;
-                                const int lo = max(0, -x0), n = min(32, it.fresh - x0);
-                                if (lo < n) {
-#pragma unroll
-                                    for (int c = 0; c < 32; ++c)
-                                        if (c >= lo && c < n) bits |= (__ldg(mr + c) != 0 ? 1u : 0u) << c;
-                                }
-                            }
-                        }
-                        bars->vis[w][threadIdx.x] = bits;
-                    }
-                }
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[b], ph(n)))) {
+                const uint32_t sb = tmem + lane_base + b * 128 + kw * CW;
+                const bool masked = k0 + CW > open;
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[b], sb_ph(n)))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t bad = bars->bad[(n / SPT) & 15];
-                // First pass over the scores: the maximum.  (The passes read the scores from
-                // TMEM 32 or 64 at a time in loops: unrolled over a row's 128 the code took
-                // 4 us to come in from memory at a kernel's first tile, against 1.1 us a tile
-                // once there.)  Hidden scores become -inf in TMEM, so that one masking serves
-                // both passes.
+                // The row's visible ones of 32 keys (held keys all are).
+                auto visible = [&](int w) -> uint32_t {
+                    const int x0 = k0 + w * 32 - it.past;  // new key of bit 0
+                    uint32_t bits = 0u;
+                    if (!masked) {
+                        bits = 0xffffffffu;
+                    } else if (!live) {
+                    } else if (p.tree == nullptr) {
+                        const int c = tok + 1 - x0;        // keys up to the row's token
+                        bits = c >= 32 ? 0xffffffffu : (c <= 0 ? 0u : (1u << c) - 1u);
+                    } else if (p.T <= 128) {
+                        const uint32_t *mr = bars->mask[masks & 1] + (tok - it.tok0) * 4;
+                        const int q = x0 >> 5, nw = (it.fresh + 31) >> 5;  // (floor)
+                        const uint32_t lo = q < 0 ? 0xffffffffu : (q < nw ? mr[q] : 0u);
+                        const uint32_t hi = q + 1 < 0 ? 0xffffffffu : (q + 1 < nw ? mr[q + 1] : 0u);
+                        bits = __funnelshift_r(lo, hi, x0 & 31);
+                    } else {
+                        bits = x0 >= 0 ? 0u : (x0 <= -32 ? 0xffffffffu : (1u << -x0) - 1u);
+                        const uint8_t *mr = p.tree + it.b * p.tree_sb + (long long)tok * p.T + x0;
+                        const int lo = max(0, -x0), hi = min(32, it.fresh - x0);
+                        for (int c = lo; c < hi; ++c) bits |= (__ldg(mr + c) != 0 ? 1u : 0u) << c;
+                    }
+                    if (bad) {  // keys of pages outside the cache are not visible
+                        const int sh = min(p.pt.page_shift, 7), sub = min(1 << sh, 32);
+                        for (int c = 0; c < 32; c += sub)
+                            if ((bad >> ((kt + w * 32 + c) >> sh)) & 1u)
+                                bits &= ~((sub == 32 ? 0xffffffffu : (1u << sub) - 1u) << c);
+                    }
+                    return bits;
+                };
+                // The maximum.  Up to 64 scores stay in registers; 128 are read from TMEM in two
+                // passes, 64 and 32 at a time in loops: unrolled, the code took 4 us to come in
+                // from memory at a kernel's first tile, against 1.1 us a tile once there.
+                // Hidden scores become -inf (in TMEM where they are read again).
+                constexpr bool HELD = CW <= 64;
+                constexpr int N = HELD ? CW : 64;
+                uint32_t sc[N];
                 float mxv[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mxv[e] = -INFINITY;
-                if (masked || bad != 0) {
 #pragma unroll 1
-                    for (int w = 0; w < CW / 32; ++w) {
-                        uint32_t bits = masked ? bars->vis[w][threadIdx.x] : 0xffffffffu;
-                        if (bad) {  // keys of pages outside the cache are not visible
-                            const int sh = min(p.pt.page_shift, 7), sub = min(1 << sh, 32);
-                            for (int c = 0; c < 32; c += sub)
-                                if ((bad >> ((kt + w * 32 + c) >> sh)) & 1u)
-                                    bits &= ~((sub == 32 ? 0xffffffffu : (1u << sub) - 1u) << c);
+                for (int w = 0; w < CW / N; ++w) {
+                    tmem_ldn<N>(sb + w * N, sc);
+                    if (HELD) {
+                        tc_fence_before();
+                        mbar_arrive(&bars->s_empty[b]);
+                    }
+                    if (masked || bad != 0) {
+#pragma unroll
+                        for (int v = 0; v < N / 32; ++v) {
+                            const uint32_t bits = visible(w * (N / 32) + v);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!((bits >> c) & 1u)) sc[v * 32 + c] = 0xff800000u;
                         }
-                        uint32_t rr[32];
-                        tmem_ld32(sb + w * 32, rr);
+                        if constexpr (!HELD) {
+                            uint32_t lo[32], hi[32];
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!((bits >> c) & 1u)) rr[c] = 0xff800000u;
-                        tmem_st32(sb + w * 32, rr);
-#pragma unroll
-                        for (int c = 0; c < 32; c += 8)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                mxv[e] = fmax3(mxv[e], __uint_as_float(rr[c + e]), __uint_as_float(rr[c + 4 + e]));
+                            for (int c = 0; c < 32; ++c) lo[c] = sc[c], hi[c] = sc[32 + c];
+                            tmem_st32(sb + w * N, lo);
+                            tmem_st32(sb + w * N + 32, hi);
+                        }
                     }
-                } else {
-                    constexpr int N = CW < 64 ? CW : 64;
-#pragma unroll 1
-                    for (int w = 0; w < CW / N; ++w) {
-                        uint32_t rr[N];
-                        tmem_ldn<N>(sb + w * N, rr);
 #pragma unroll
-                        for (int c = 0; c < N; c += 8)
+                    for (int c = 0; c < N; c += 8)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                mxv[e] = fmax3(mxv[e], __uint_as_float(rr[c + e]), __uint_as_float(rr[c + 4 + e]));
-                    }
+                        for (int e = 0; e < 4; ++e)
+                            mxv[e] = fmax3(mxv[e], __uint_as_float(sc[c + e]), __uint_as_float(sc[c + 4 + e]));
                 }
                 const float mx = fmaxf(fmax3(mxv[0], mxv[1], mxv[2]), mxv[3]) * sl2;
                 // Lazy rescale: m moves when the maximum grew by more than 2^8.
@@ -760,16 +808,14 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     m = mx;
                 }
                 const float m_use = (m == -INFINITY) ? 0.f : m;
-                // P's buffer is free once P V of step n - 2 is done (where P overwrites S it
-                // is: the wait keeps the phases in order); O may be rescaled once that of step
-                // n - 1 is.
-                if (n >= 2 &&
-                    !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[b], ph(n - 2)))) {
+                // P's buffer is free once P V of step n - 2 is done; O may be rescaled once that
+                // of step n - 1 is.
+                if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[pb_of(n, ti)], pb_ph(n - 2)))) {
                     ok = false;
                     break;
                 }
                 if (i > 0 && any_grow) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[bi(n - 1, ti)], ph(n - 1)))) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[pb_of(n - 1, ti)], pb_ph(n - 1)))) {
                         ok = false;
                         break;
                     }
@@ -784,15 +830,15 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     }
                 }
                 tc_fence_after();
-                // Second pass: the weights, their sums, P.  (P overwrites S behind the reads.)
+                // The weights, their sums, P.
                 float2 ls = make_float2(0.f, 0.f), rs = make_float2(0.f, 0.f);
-                const float2 sc = make_float2(sl2, sl2), nm = make_float2(-m_use, -m_use);
-                const uint32_t pb = C::P_OWN ? tmem + lane_base + C::COL_P + (n & 1) * C::P_STEP + kw * (CW / 2) : sb;
-                auto weights = [&](const uint32_t (&rr)[32], uint32_t dst) {
+                const float2 sc2 = make_float2(sl2, sl2), nm = make_float2(-m_use, -m_use);
+                const uint32_t pb = tmem + lane_base + C::COL_P + ti * C::S_TILE + (n & 1) * C::P_BUF + kw * (CW / 2);
+                auto weights = [&](const uint32_t *rr, uint32_t dst) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        const float2 x = fma2(make_float2(__uint_as_float(rr[c]), __uint_as_float(rr[c + 1])), sc, nm);
+                        const float2 x = fma2(make_float2(__uint_as_float(rr[c]), __uint_as_float(rr[c + 1])), sc2, nm);
                         const float2 w = make_float2(ex2(x.x), ex2(x.y));
                         ls = add2(ls, w);
                         pk[c >> 1] = pack2<BF16>(w.x, w.y);
@@ -800,37 +846,41 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     }
                     tmem_st16_async(dst, pk);
                 };
-                {
+                if constexpr (HELD) {
+#pragma unroll
+                    for (int w = 0; w < CW / 32; ++w) weights(sc + w * 32, pb + w * 16);
+                } else {
                     uint32_t ra[32], rb[32];
                     tmem_ld32(sb, ra);
-                    if constexpr (CW == 32) {
-                        weights(ra, pb);
-                    } else {
 #pragma unroll 1
-                        for (int w = 0; w < CW / 32; w += 2) {  // the next 32 are on their way
-                            tmem_ld32_async(sb + (w + 1) * 32, rb);
-                            weights(ra, pb + w * 16);
-                            tmem_wait_ld(rb);
-                            // (behind the last: a load that nobody uses, so that the loop's
-                            // registers are not merged before the wait)
-                            tmem_ld32_async(sb + min(w + 2, CW / 32 - 1) * 32, ra);
-                            weights(rb, pb + (w + 1) * 16);
-                            tmem_wait_ld(ra);
-                        }
+                    for (int w = 0; w < CW / 32; w += 2) {  // the next 32 are on their way
+                        tmem_ld32_async(sb + (w + 1) * 32, rb);
+                        weights(ra, pb + w * 16);
+                        tmem_wait_ld(rb);
+                        // (behind the last: a load that nobody uses, so that the loop's
+                        // registers are not merged before the wait)
+                        tmem_ld32_async(sb + min(w + 2, CW / 32 - 1) * 32, ra);
+                        weights(rb, pb + (w + 1) * 16);
+                        tmem_wait_ld(ra);
                     }
-                    tmem_wait_st();
                 }
+                tmem_wait_st();
                 l = l * alpha + (ls.x + ls.y);
                 lr = lr * alpha + (rs.x + rs.y);
                 tc_fence_before();
-                if (C::P_OWN) mbar_arrive(&bars->s_empty[b]);
-                mbar_arrive(&bars->p_full[b]);
+                if (!HELD) mbar_arrive(&bars->s_empty[b]);
+                mbar_arrive(&bars->p_full[pb_of(n, ti)]);
             }
 
+            if (bits_used) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->mask_empty[masks & 1]);
+                ++masks;
+            }
             // ------------------------------ epilogue of the piece ------------------------
             if (ok && nt > 0) {
                 const int n = n0 + nt * SPT - 1;
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[bi(n, ti)], ph(n)));
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[pb_of(n, ti)], pb_ph(n)));
                 tc_fence_after();
             }
             // (the merge of the copies has barriers of all four warps: they leave together)
@@ -843,7 +893,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             float lse2 = none ? -INFINITY : m + lg2(l);
             // Values that the repair cleared reach the rows that do see them (rare: only where
             // a new key's V is not finite, and slow).
-            const bool poison = nt > 0 && it.hides(p) && it.j1 * 128 > it.past && bars->poison[t & 3] != 0;
+            const bool poison = nt > 0 && it.repair(p, it.j1 - 1) && bars->poison[t & 3] != 0;
             auto add_not_finite = [&](float *v, int n, int col, int tk) {
                 for (int j = max(it.past, it.j0 * 128); j < min(it.total, it.j1 * 128); ++j) {
                     const int x = j - it.past;
