@@ -69,18 +69,24 @@ struct PagedCfg {
     static constexpr int QTILE = 128 * D * 2;
     static constexpr int TILE = BN * D * 2;     // K or V tile
     static constexpr int HALF = BN * 128;       // one 64-element column block of a tile
-    static constexpr int NS = (D == 64) ? (RT == 1 ? 11 : 10) : (RT == 1 ? 5 : 4);  // K, V ring
+    // rings of K and V tiles (V, used later, has the odd slot: 62 -> 56 us for decoding 32K
+    // keys at d = 64 from pages of 16)
+    static constexpr int NK = (D == 64) ? 5 : 2;
+    static constexpr int NV = (D == 64) ? (RT == 1 ? 6 : 5) : (RT == 1 ? 3 : 2);
     // epilogue: REP > 1, a 32-column block of every row and copy, rows padded to 36 columns;
     // else 32 rows x 32 columns of 16 bits for each warp
     static constexpr int MERGE = (REP > 1) ? 128 * 36 * 4 : RT * 4 * 2048;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + RT * QTILE;
-    static constexpr int OFF_MERGE = OFF_RING + NS * TILE;
+    static constexpr int OFF_MERGE = OFF_RING + (NK + NV) * TILE;
     static constexpr int OFF_BAR = OFF_MERGE + MERGE;
     static constexpr int USED = OFF_BAR + 3072 + 8192;
     static constexpr int SMEM = USED + 1024;
     static constexpr int SOFT = 4 * RT;         // softmax warps
-    static constexpr int THREADS = 32 * (SOFT + 4);
+    // K and V come from a warp each where the registers allow one more: a box takes about
+    // 45 ns to issue, and pages of 16 tokens are 32 boxes a tile at d = 128.
+    static constexpr int LOADERS = (RT == 1) ? 2 : 1;
+    static constexpr int THREADS = 32 * (SOFT + 3 + LOADERS);
     // The softmax goes in steps: whole tiles (RT = 1) or 64 keys (RT = 2), whose scores a
     // thread holds in registers, so that the one score buffer that TMEM has room for at
     // d = 128 is free for the next step's S at once.  (A chunk of 512 tokens against 16K keys,
@@ -107,11 +113,10 @@ struct PagedBars {
     uint64_t need[4];
     uint64_t s_full[2], s_empty[2];   // index: score buffer (RT = 1) or row tile
     uint64_t p_full[4], pv_done[4];   // index: 2 * row tile + buffer of P
-    // Fills are announced per tile (mod 8; a ring holds at most 6), K and V apart, so that
-    // each is waited for in order by the issuer that uses it; a ring slot, which K and V may
-    // take in turn, is released per slot.  fixed: V repaired.
+    // Fills are announced per tile (mod 8; a ring holds at most 6), slots released per slot.
+    // fixed: V repaired.
     uint64_t kfull[8], vfull[8], fixed[8];
-    uint64_t empty[12];
+    uint64_t kempty[6], vempty[6];
     uint64_t seg_full[4], seg_empty[4];
     uint64_t mask_full[2], mask_empty[2];
     uint32_t tmem_base;
@@ -125,9 +130,9 @@ struct PagedBars {
 };
 
 // Work units of a sequence: for each of its items with a new token the key tiles and kItemCost
-// for what an item costs by itself (its first scores, its epilogue: 1 to 2 us against 0.8 to
-// 1.5 us a tile), one for an item without (its rows are written as empty).
-constexpr int kItemCost = 1;
+// for what an item costs by itself (its first scores, its epilogue: about 4 us against 1 to
+// 1.5 us a tile; 16 ragged sequences with trees of 16 tokens: 69, 64, 60 us at 1, 2, 3), one for an item without (its rows are written as empty).
+constexpr int kItemCost = 3;
 struct PagedSeq {
     int past, fresh, tiles, valid;  // valid: items that hold a new token
     int per_head;
@@ -219,7 +224,8 @@ struct PagedWalk {
             mine = sq.per_head * p.Hk;
         }
     }
-    __device__ __forceinline__ void init(const PagedParams &p, int lane) {
+    // Share c of all units; returns the shares.
+    __device__ __forceinline__ PagedShares init(const PagedParams &p, int c, int lane) {
         int W = 0;
         for (int k = 0; k < p.B; k += 32) {
             load(p, k, lane);
@@ -227,14 +233,38 @@ struct PagedWalk {
         }
         PagedShares sh;
         sh.init(W, p.ctas);
-        u = min(sh.begin(blockIdx.x), W);
-        u1 = min(sh.begin(blockIdx.x + 1), W);
+        u = min(sh.begin(c), W);
+        u1 = min(sh.begin(c + 1), W);
         if (p.B > 32) load(p, 0, lane);
         base = 0;
         upto = warp_scan(mine, lane);
         n = 0;
         first = true;
         done = false;
+        return sh;
+    }
+    // The sequence with unit u, and u's place in its head `hk` (u must not go back).
+    struct Place {
+        int b, hk, r, past, fresh, tiles, valid;
+    };
+    __device__ __forceinline__ Place place(const PagedParams &p, int lane) {
+        for (int all; base + (all = __shfl_sync(0xffffffffu, upto, 31)) <= u;) {
+            base += all;
+            load(p, k0 + 32, lane);
+            upto = warp_scan(mine, lane);
+        }
+        Place x;
+        const int f = __ffs(__ballot_sync(0xffffffffu, base + upto > u)) - 1;
+        const int r0 = u - base - __shfl_sync(0xffffffffu, upto - mine, f);
+        const int per_head = __shfl_sync(0xffffffffu, sq.per_head, f);
+        x.b = k0 + f;
+        x.past = __shfl_sync(0xffffffffu, sq.past, f);
+        x.fresh = __shfl_sync(0xffffffffu, sq.fresh, f);
+        x.tiles = __shfl_sync(0xffffffffu, sq.tiles, f);
+        x.valid = __shfl_sync(0xffffffffu, sq.valid, f);
+        x.hk = (unsigned)r0 / (unsigned)per_head;
+        x.r = r0 - x.hk * per_head;
+        return x;
     }
     // The next piece goes to the ring (b = -1 after the last); false if a wait gave up.
     __device__ __forceinline__ bool step(const PagedParams &p, PagedBars *bars, int lane) {
@@ -242,21 +272,12 @@ struct PagedWalk {
         PagedSeg g;
         g.b = -1;
         while (u < u1) {
-            for (int all; base + (all = __shfl_sync(0xffffffffu, upto, 31)) <= u;) {
-                base += all;
-                load(p, k0 + 32, lane);
-                upto = warp_scan(mine, lane);
-            }
-            const int f = __ffs(__ballot_sync(0xffffffffu, base + upto > u)) - 1;
-            const int r0 = u - base - __shfl_sync(0xffffffffu, upto - mine, f);
-            const int per_head = __shfl_sync(0xffffffffu, sq.per_head, f);
-            const int tiles = __shfl_sync(0xffffffffu, sq.tiles, f);
-            const int valid = __shfl_sync(0xffffffffu, sq.valid, f);
-            g.past = __shfl_sync(0xffffffffu, sq.past, f);
-            g.fresh = __shfl_sync(0xffffffffu, sq.fresh, f);
+            const Place x = place(p, lane);
+            const int r = x.r, tiles = x.tiles, valid = x.valid;
+            g.past = x.past;
+            g.fresh = x.fresh;
             g.total = g.past + g.fresh;
-            g.hk = (unsigned)r0 / (unsigned)per_head;
-            const int r = r0 - g.hk * per_head;
+            g.hk = x.hk;
             const int cost = tiles + kItemCost;
             g.slot = 2 * blockIdx.x + (first ? 0 : 1);
             first = false;
@@ -281,7 +302,7 @@ struct PagedWalk {
                 g.whole = 1;
                 u += 1;
             }
-            g.b = k0 + f;
+            g.b = x.b;
             const int tt = p.GT == 1 ? rt : rt / p.GT;
             g.tok0 = tt * RT * p.TPT;
             g.g0 = p.GT == 1 ? 0 : (rt - tt * p.GT) * p.GP;
@@ -385,7 +406,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     constexpr int ROWS = C::ROWS;
     constexpr int CW = C::STEP / REP; // keys of a step that one thread handles
     constexpr int SPT = C::SPT;
-    constexpr int W_TMA = C::SOFT, W_S = C::SOFT + 1, W_PV = C::SOFT + 2, W_FIX = C::SOFT + 3;
+    constexpr int W_S = C::SOFT, W_PV = C::SOFT + 1, W_FIX = C::SOFT + 2, W_TMA = C::SOFT + 3;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sQ = smem + C::OFF_Q;
@@ -427,10 +448,13 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             mbar_init(&bars->vfull[i], 1);
             mbar_init(&bars->fixed[i], 1);
         }
-        for (int i = 0; i < C::NS; ++i) mbar_init(&bars->empty[i], 1);
+        for (int i = 0; i < 6; ++i) {
+            mbar_init(&bars->kempty[i], 1);
+            mbar_init(&bars->vempty[i], 1);
+        }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars->seg_full[i], 1);
-            mbar_init(&bars->seg_empty[i], C::SOFT + 4);
+            mbar_init(&bars->seg_empty[i], C::SOFT + 3 + C::LOADERS);
         }
         fence_mbar_init();
     }
@@ -450,53 +474,58 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     PagedSeg it;
     int np = 0;  // pieces taken
 
-    if (warp == W_TMA) {
-        // ------------------------------ K and V: whole warp -----------------------------
+    if (warp >= W_TMA) {
+        // ------------------------------ K and V: a whole warp each ----------------------
         // A tile's pages: npt boxes (a page, or 128 rows of a larger one) per 64-element
-        // column block; lane l loads box l % npt of block l / npt.
+        // column block; lane l loads box l % npt of block l / npt.  Page numbers are read one
+        // tile ahead.
+        const int kv0 = C::LOADERS == 2 ? warp - W_TMA : 0, kv1 = C::LOADERS == 2 ? kv0 + 1 : 2;
         const int page = 1 << p.pt.page_shift;
         const int box_rows = min(page, 128);
         const int npt = 128 / box_rows;
         const int mine = lane % npt, half = lane / npt;
-        int gj = 0, fills = 0;  // tiles and fills so far
+        int gj = 0;  // tiles so far
         bool ok = true;
         while (ok && paged_take(bars, np++, lane, true, it)) {
             const int *row = p.pt.table + (long long)it.b * p.pt.max_blocks;
-            for (int j = it.j0; j < it.j1; ++j, ++gj) {
+            auto page_at = [&](int j) -> int {  // (a place behind the last key: -1)
                 const int key = j * 128 + mine * box_rows;
-                int z = p.pt.num_pages;  // outside the cache: the box is filled with zeros
-                bool bad = false;
-                if (key < it.total) {
-                    const int id = __ldg(row + (key >> p.pt.page_shift));
-                    bad = id < 0 || id >= p.pt.num_pages;
-                    if (!bad) z = id;
-                }
-                const unsigned bads = __ballot_sync(0xffffffffu, bad && half == 0);
-                if (lane == 0) {
-                    bars->bad[gj & 15] = bads;
-                    if (bads) atomicExch(&g_status, 6);
+                return key < it.total ? __ldg(row + (key >> p.pt.page_shift)) : -1;
+            };
+            int next = page_at(it.j0);
+            for (int j = it.j0; ok && j < it.j1; ++j, ++gj) {
+                const int key = j * 128 + mine * box_rows, id = next;
+                if (j + 1 < it.j1) next = page_at(j + 1);
+                const bool bad = key < it.total && (id < 0 || id >= p.pt.num_pages);
+                // outside the cache: the box is filled with zeros
+                const int z = key < it.total && !bad ? id : p.pt.num_pages;
+                if (kv0 == 0) {
+                    const unsigned bads = __ballot_sync(0xffffffffu, bad && half == 0);
+                    if (lane == 0) {
+                        bars->bad[gj & 15] = bads;
+                        if (bads) atomicExch(&g_status, 6);
+                    }
                 }
                 const int y = key & (page - 1);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const int n = 2 * gj + kv, s = n % C::NS;
-                    if (n >= C::NS)
-                        ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[s], (n / C::NS - 1) & 1));
+                for (int kv = kv0; kv < kv1; ++kv) {
+                    const int N = kv ? C::NV : C::NK, s = gj % N;
+                    if (gj >= N)
+                        ok = __all_sync(0xffffffffu,
+                                        mbar_wait(kv ? &bars->vempty[s] : &bars->kempty[s], (gj / N - 1) & 1));
                     if (!ok) break;
                     uint64_t *full = kv ? &bars->vfull[gj & 7] : &bars->kfull[gj & 7];
                     if (lane == 0) mbar_arrive_expect_tx(full, C::TILE);
                     __syncwarp();
                     if (half < C::HALVES)
-                        tma_load_4d(ring + s * C::TILE + half * C::HALF + mine * box_rows * 128,
+                        tma_load_4d(ring + (kv ? C::NK + s : s) * C::TILE + half * C::HALF + mine * box_rows * 128,
                                     kv ? &tmV : &tmK, full, half * 64, y, it.hk, z);
-                    ++fills;
                 }
-                if (!ok) break;
             }
         }
         if (!ok)  // a wait gave up: the copies in flight land before the CTA's memory goes
-            for (int n = max(0, fills - C::NS); n < fills; ++n)
-                (void)mbar_wait(n & 1 ? &bars->vfull[(n >> 1) & 7] : &bars->kfull[(n >> 1) & 7], (n >> 4) & 1);
+            for (int kv = kv0; kv < kv1; ++kv)
+                for (int g = max(0, gj - 6); g < gj; ++g)
+                    (void)mbar_wait(kv ? &bars->vfull[g & 7] : &bars->kfull[g & 7], (g >> 3) & 1);
     } else if (warp == W_S) {
         // ------------------------------ issuer of S -------------------------------------
         if (lane == 0) {
@@ -512,7 +541,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 if (!mbar_wait(&bars->q_full, t & 1)) break;
                 for (int x = 0; ok && x < steps; ++x) {
                     const int n = n0 + x, h = x % SPT;
-                    const int g = n / SPT, s = 2 * g % C::NS;  // tile, K's slot
+                    const int g = n / SPT, s = g % C::NK;  // tile, K's slot
                     if (h == 0 && !mbar_wait(&bars->kfull[g & 7], (g >> 3) & 1)) { ok = false; break; }
                     const uint64_t kd = k_desc + (uint64_t)((s * C::TILE + h * C::STEP * 128) >> 4);
 #pragma unroll
@@ -532,7 +561,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         }
                         // (the barriers that nobody waits for at the end come first, so that no
                         // arrival is outstanding when the CTA ends)
-                        if (i == RT - 1 && h == SPT - 1) mma_commit(&bars->empty[s]);
+                        if (i == RT - 1 && h == SPT - 1) mma_commit(&bars->kempty[s]);
                         if (i == RT - 1 && x == steps - 1) mma_commit(&bars->q_empty);
                         mma_commit(&bars->s_full[b]);
                     }
@@ -556,7 +585,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 if (steps <= 0) continue;
                 for (int x = 0; ok && x < steps; ++x) {
                     const int n = n0 + x, h = x % SPT;
-                    const int g = n / SPT, s = (2 * g + 1) % C::NS;  // tile, V's slot
+                    const int g = n / SPT, s = C::NK + g % C::NV;  // tile, V's slot
                     if (h == 0) {
                         if (!mbar_wait(&bars->vfull[g & 7], (g >> 3) & 1)) { ok = false; break; }
                         if (it.repair(p, it.j0 + x / SPT)) {
@@ -576,7 +605,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         for (int kk = 0; kk < C::STEP / 16; ++kk)
                             mma_ts(tmem + C::COL_O + i * D, pa + kk * 8,
                                    vd + (uint64_t)((kk * 16 * 128) >> 4), kIdesc, x > 0 || kk > 0);
-                        if (i == RT - 1 && h == SPT - 1) mma_commit(&bars->empty[s]);
+                        if (i == RT - 1 && h == SPT - 1) mma_commit(&bars->vempty[g % C::NV]);
                         mma_commit(&bars->pv_done[b]);
                     }
                 }
@@ -587,7 +616,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     } else if (warp == W_FIX) {
         // ------------------------------ pieces, Q loads, V repairs ----------------------
         PagedWalk<RT> walk;
-        walk.init(p, lane);
+        walk.init(p, blockIdx.x, lane);
         bool ok = walk.step(p, bars, lane) && walk.step(p, bars, lane);
         if (blockIdx.x == 0)
             for (int b = lane; b < p.B; b += 32) page_lengths_check(p.pt, p.T, b);
@@ -635,7 +664,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             for (int i = 0; ok && i < nt; ++i) {
                 const int j = it.j0 + i;
                 if (!it.repair(p, j)) continue;
-                const int g = gj + i, s = (2 * g + 1) % C::NS;
+                const int g = gj + i, s = C::NK + g % C::NV;
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars->need[served & 3], (served >> 2) & 1) &&
                                                  mbar_wait(&bars->vfull[g & 7], (g >> 3) & 1));
                 if (!ok) break;
@@ -1076,37 +1105,35 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 
 // Merges the pieces of the items that were cut: with the pieces' log-sum-exps L_s (base 2),
 //   LSE = M + log2 sum_s 2^(L_s - M), O = sum_s 2^(L_s - LSE) O_s.
-// The pieces and their places are worked out before the wait for the attention kernel (which
+// A share leaves at most one item unfinished that it began: grid.x = shares.  The item, its
+// pieces and their places are worked out before the wait for the attention kernel (which
 // triggers this launch behind its own wait, so that the lengths are final by then).
-// TRANS (rows of a piece as [column / 4][row]): grid = (items, groups of 32 rows), a lane is
-// a row, a warp 1 / 8 of the columns.  Else: grid = (items, groups of 16 rows), a warp is a
-// row at a time, a lane 1 / 32 of the columns.
+// TRANS (rows of a piece as [column / 4][row]): grid.y = groups of 32 rows, a lane is a row, a
+// warp 1 / 8 of the columns.  Else: groups of 16 rows, a warp is a row at a time, a lane 1 / 32
+// of the columns.
 template <int D, bool BF16, int RT, bool TRANS>
 __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_constant__ PagedParams p,
                                                              const int rows) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int item = blockIdx.x;
-    const int rt = item % p.row_tiles, hk = (item / p.row_tiles) % p.Hk, b = item / p.row_tiles / p.Hk;
-    const PagedSeq s = paged_seq<RT>(p, b);
-    bool cut = rt < s.valid;
-    int c0 = 0, c1 = 0, first = 0;
-    if (cut) {
-        int W = 0, base = 0;  // all units, those before the sequence
-        for (int k = lane; k < p.B; k += 32) {
-            const int n = paged_seq<RT>(p, k).per_head * p.Hk;
-            W += n;
-            base += k < b ? n : 0;
+    const int c0 = blockIdx.x;
+    PagedWalk<RT> walk;
+    const PagedShares sh = walk.init(p, c0, lane);
+    bool cut = false;
+    int b = 0, hk = 0, rt = 0, c1 = 0, first = 0;
+    if (walk.u < walk.u1) {
+        const int begin = walk.u, end = walk.u1;
+        walk.u = end - 1;
+        const auto x = walk.place(p, lane);
+        const int cost = x.tiles + kItemCost;
+        if (x.r < x.valid * cost) {
+            rt = (unsigned)x.r / (unsigned)cost;
+            const int u0 = end - 1 - (x.r - rt * cost);  // the item's first unit
+            cut = u0 >= begin && u0 + x.tiles > end;
+            b = x.b;
+            hk = x.hk;
+            c1 = sh.of(u0 + x.tiles - 1);
+            first = begin < u0 ? 1 : 0;  // (its first piece is not the share's first)
         }
-        W = warp_sum(W);
-        base = warp_sum(base);
-        PagedShares sh;
-        sh.init(W, p.ctas);
-        const int u0 = base + hk * s.per_head + rt * (s.tiles + kItemCost);
-        c0 = sh.of(u0);
-        c1 = sh.of(u0 + s.tiles - 1);
-        cut = c0 != c1;
-        // the first piece lies in CTA c0's second slot if that share began before the item
-        first = sh.begin(c0) < u0 ? 1 : 0;
     }
     pdl_wait();
     pdl_launch_dependents();
