@@ -873,10 +873,10 @@ int launch_paged(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap
     if (e == cudaSuccess && !p.uncut) {
         constexpr bool TRANS = REP == 1;
         // rows in use: all of an item's, or those of the call's tokens where these are fewer
-        const int rows = RT == 2 ? 256 : std::min(p.TPT, p.T) * p.GP, per = TRANS ? 32 : 16;
+        const int rows = RT == 2 ? 256 : std::min(p.TPT, p.T) * p.GP;
         e = launch_pdl(fa::fa_paged_merge_kernel<D, BF16, RT, TRANS>,
-                       dim3((unsigned)p.ctas, (unsigned)((rows + per - 1) / per)),
-                       dim3(256), 0, st, p, (int)C::ROWS);
+                       dim3((unsigned)p.ctas, (unsigned)((rows + 31) / 32)), dim3(256), 0, st, p,
+                       (int)C::ROWS);
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {

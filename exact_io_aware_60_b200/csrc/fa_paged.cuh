@@ -1109,13 +1109,13 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 // pieces and their places are worked out before the wait for the attention kernel (which
 // triggers this launch behind its own wait, so that the lengths are final by then).
 // TRANS (rows of a piece as [column / 4][row]): grid.y = groups of 32 rows, a lane is a row, a
-// warp 1 / 8 of the columns.  Else: groups of 16 rows, a warp is a row at a time, a lane 1 / 32
-// of the columns.
+// warp 1 / 8 of the columns.  Else: a warp is a row at a time, a lane 1 / 32 of the columns.
 template <int D, bool BF16, int RT, bool TRANS>
 __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_constant__ PagedParams p,
                                                              const int rows) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = blockIdx.x;
+    pdl_launch_dependents();  // (whoever comes next waits for this grid's end in its turn)
     PagedWalk<RT> walk;
     const PagedShares sh = walk.init(p, c0, lane);
     bool cut = false;
@@ -1136,54 +1136,59 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
         }
     }
     pdl_wait();
-    pdl_launch_dependents();
     if (!cut) return;
-    constexpr int NR = TRANS ? 1 : 2;  // rows of a thread
-#pragma unroll 1
+    // Each round takes four pieces, log-sum-exps and outputs together, into a running maximum
+    // and sum: one wait on L2 (about 0.7 us) a round.
+    constexpr int NR = TRANS ? 1 : 4;          // rows of a thread in a group of 32
+    constexpr int E = TRANS ? D / 8 : D / 32;  // columns of a thread
+    constexpr int U = 4;
+#pragma unroll 2
     for (int k = 0; k < NR; ++k) {
-        const int row = TRANS ? blockIdx.y * 32 + lane : blockIdx.y * 16 + k * 8 + warp;  // of the item
+        const int row = blockIdx.y * 32 + (TRANS ? lane : k * 8 + warp);  // of the item
         const int tile = row / rows, r = row - tile * rows;
         const int tl = r * p.gp_magic >> 16, tt = rt / p.GT;
         const int tok = (tt * RT + tile) * p.TPT + tl, head = (rt - tt * p.GT) * p.GP + (r - tl * p.GP);
         if (tile >= RT || tl >= p.TPT || tok >= p.T || head >= p.G) continue;
-        auto at = [&](int c) -> long long { return (2LL * c + (c == c0 ? first : 0)) * (RT * rows); };
-        float M = -INFINITY;
-        if constexpr (TRANS) {
-#pragma unroll 8
-            for (int c = c0; c <= c1; ++c) M = fmaxf(M, p.part_lse[at(c) + row]);
-        } else {
-            for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_lse[at(c) + row]);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        }
-        constexpr int E = TRANS ? D / 8 : D / 32;  // columns of a thread
-        float acc[E], sum = 0.f;
+        float acc[E], sum = 0.f, M = -INFINITY;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll TRANS ? 2 : 8
-        for (int c = c0; c <= c1; ++c) {
-            const float ls = p.part_lse[at(c) + row];
-            const float w = ls == -INFINITY ? 0.f : ex2(ls - M);
-            sum += w;
-            if constexpr (TRANS) {
-                const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (at(c) + tile * rows) * D) +
-                                    warp * (E / 4) * rows + r;
+        for (int s0 = c0; s0 <= c1; s0 += U) {
+            float ls[U], v[U][E];
 #pragma unroll
-                for (int e = 0; e < E / 4; ++e) {
-                    const float4 x = src[e * rows];
-                    acc[4 * e] = fmaf(w, x.x, acc[4 * e]);
-                    acc[4 * e + 1] = fmaf(w, x.y, acc[4 * e + 1]);
-                    acc[4 * e + 2] = fmaf(w, x.z, acc[4 * e + 2]);
-                    acc[4 * e + 3] = fmaf(w, x.w, acc[4 * e + 3]);
-                }
-            } else {
-                const float2 *src = reinterpret_cast<const float2 *>(p.part_o + (at(c) + row) * D + lane * E);
+            for (int u = 0; u < U; ++u) {
+                const int c = min(s0 + u, c1);
+                const long long at = (2LL * c + (c == c0 ? first : 0)) * (RT * rows);
+                ls[u] = s0 + u <= c1 ? p.part_lse[at + row] : -INFINITY;
+                if constexpr (TRANS) {
+                    const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (at + tile * rows) * D) +
+                                        warp * (E / 4) * rows + r;
 #pragma unroll
-                for (int e = 0; e < E / 2; ++e) {
-                    const float2 x = src[e];
-                    acc[2 * e] = fmaf(w, x.x, acc[2 * e]);
-                    acc[2 * e + 1] = fmaf(w, x.y, acc[2 * e + 1]);
+                    for (int e = 0; e < E / 4; ++e) {
+                        const float4 x = src[e * rows];
+                        v[u][4 * e] = x.x, v[u][4 * e + 1] = x.y, v[u][4 * e + 2] = x.z, v[u][4 * e + 3] = x.w;
+                    }
+                } else if constexpr (E == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(p.part_o + (at + row) * D + lane * E);
+                    v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2 *>(p.part_o + (at + row) * D + lane * E);
+                    v[u][0] = x.x, v[u][1] = x.y;
                 }
+            }
+            float M1 = M;
+#pragma unroll
+            for (int u = 0; u < U; ++u) M1 = fmaxf(M1, ls[u]);
+            const float alpha = M == -INFINITY ? 0.f : ex2(M - M1);
+            M = M1;
+            sum *= alpha;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= alpha;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float w = ls[u] == -INFINITY ? 0.f : ex2(ls[u] - M1);  // (NaN is carried on)
+                sum += w;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[u][e], acc[e]);
             }
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -1192,7 +1197,7 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
                                                    tok * p.o.st + (TRANS ? warp : lane) * E);
         uint32_t w[E / 2];
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) w[e] = pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        for (int e = 0; e < E / 2; ++e) w[e] = sum == 0.f ? 0u : pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
         if constexpr (E / 2 >= 4) {
 #pragma unroll
             for (int e = 0; e < E / 8; ++e)
