@@ -1,4 +1,5 @@
-"""Builds libfa.so (the C-ABI attention library) in-tree with nvcc for sm_100a.
+"""Builds libfa.so (the C-ABI attention library) in-tree with nvcc for sm_100a, and the quick
+binding of its serving calls (_fa_binding.so) with g++ against torch's headers.
 
 Usage:  python -m exact_io_aware_60_b200.build [--force]
 """
@@ -14,6 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfa.so")
+BINDING = os.path.join(PKG, "_fa_binding.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -41,7 +43,32 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and os.path.exists(BINDING) and os.path.getmtime(src) <= os.path.getmtime(BINDING):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+    tmp = BINDING + f".tmp{os.getpid()}"
+    libs = ext.library_paths(device_type="cuda")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(f"-I{p}" for p in ext.include_paths(device_type="cuda")),
+           f"-I{sysconfig.get_paths()['include']}", src, "-o", tmp, *(f"-L{p}" for p in libs),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed building _fa_binding.so")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force, verbose)
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"

@@ -20,6 +20,11 @@ from typing import Optional
 
 import torch
 
+try:
+    from . import _fa_binding as _quick  # (needs torch's libraries, loaded above)
+except ImportError:                      # not built: the same calls by ctypes
+    _quick = None
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfa.so")
 
@@ -31,6 +36,7 @@ FA_BF16, FA_FP16 = 0, 1
 
 _lock = threading.Lock()
 _lib = None
+_addr = {}  # of the entry points that _fa_binding calls
 
 
 class FAError(RuntimeError):
@@ -114,6 +120,8 @@ def lib():
                                        + [i, f, i, vp, sz, vp])
             L.fa_schedule_items.restype = i
             L.fa_schedule_items.argtypes = [vp, i, i, vp, vp]
+            for n in ("fa_rope", "fa_rope_bwd", "fa_kv_append", "fa_fwd_paged"):
+                _addr[n] = ctypes.cast(getattr(L, n), ctypes.c_void_p).value
             _lib = L
     return _lib
 
@@ -557,7 +565,26 @@ def _plan_args(plan, index: int):
     return turns, plan.rot_dim, int(plan.interleaved), plan.magnitude
 
 
-def _rope_call(fn, where, x, x_out, plan, y, y_out, positions, stream, names):
+def _quick_call(fn, where, *args) -> bool:
+    """A call through _fa_binding; False where it is not plain (see csrc/binding.cpp)."""
+    rc = fn(_addr.get(where) or (lib() and _addr[where]), *args)
+    if rc is None:
+        return False
+    if rc != FA_OK:
+        raise FAError(rc, where)
+    return True
+
+
+def _handle(stream):
+    return None if stream is None else int(stream.cuda_stream)
+
+
+def _rope_call(where, x, x_out, plan, y, y_out, positions, stream, names):
+    if _quick is not None and isinstance(plan, RopePlan) and _quick_call(
+            _quick.rope, where, x, x_out, y, y_out, positions, plan.turns, plan.rot_dim,
+            plan.interleaved, plan.magnitude, _handle(stream)):
+        return
+    fn = getattr(lib(), where)
     shape, dtype, index, code = _main(x, names[0])
     B, H, N, d = shape
     xs = None if x.is_contiguous() else _rows(x, names[0], shape, dtype, index)
@@ -594,7 +621,7 @@ def fa_rope(q, q_out, plan: RopePlan, *, k=None, k_out=None, positions=None, str
     """Rotary positions: writes ``q_out`` [B,H,N,d] (and ``k_out`` [B,Hk,N,d]) from ``q`` (and
     ``k``) in one launch; ``q_out`` may be ``q``.  Strided views with a contiguous last
     dimension are taken as they are.  ``positions``: int32 [N] or [B,N], None for 0 .. N-1."""
-    _rope_call((_lib or lib()).fa_rope, "fa_rope", q, q_out, plan, k, k_out, positions, stream,
+    _rope_call("fa_rope", q, q_out, plan, k, k_out, positions, stream,
                ("q", "q_out", "k", "k_out"))
 
 
@@ -602,7 +629,7 @@ def fa_rope_bwd(dq_rot, dq, plan: RopePlan, *, k=None, k_out=None, positions=Non
                 stream=None) -> None:
     """Backward pass of :func:`fa_rope`: gradients of its inputs from those of its outputs.
     ``dq_rot`` -> ``dq``, and ``k`` (the gradient of the rotated keys) -> ``k_out``."""
-    _rope_call((_lib or lib()).fa_rope_bwd, "fa_rope_bwd", dq_rot, dq, plan, k, k_out, positions, stream,
+    _rope_call("fa_rope_bwd", dq_rot, dq, plan, k, k_out, positions, stream,
                ("dq_rot", "dq", "k", "k_out"))
 
 
@@ -635,6 +662,12 @@ def fa_kv_append(k, v, k_cache, v_cache, block_table, cache_len, *, new_len=None
     of sequence b goes to slot ``cache_len[b] + t`` (see include/fa.h); the lengths are not
     advanced.  ``new_len``: int32 [B], None for T each; ``positions``: int32 [B,T], None for
     the slots' own.  Strided views with a contiguous last dimension are taken as they are."""
+    if _quick is not None and (rope is None or isinstance(rope, RopePlan)) and _quick_call(
+            _quick.append, "fa_kv_append", k, v, k_cache, v_cache, block_table, cache_len, new_len,
+            q, q_out, positions, *((None, 0, False, 1.0) if rope is None else
+                                   (rope.turns, rope.rot_dim, rope.interleaved, rope.magnitude)),
+            _handle(stream)):
+        return
     shape, dtype, index, code = _main(k, "k")
     B, Hk, T, d = shape
     ks = None if k.is_contiguous() else _rows(k, "k", shape, dtype, index)
@@ -657,7 +690,7 @@ def fa_kv_append(k, v, k_cache, v_cache, block_table, cache_len, *, new_len=None
         raise FAError(FA_ERR_INVALID_ARG, "q and q_out go together")
     pp = None if positions is None else _ints(positions, "positions", ((B, T),), index)
     turns, rot, inter, mag = (None, 0, 0, 1.0) if rope is None else _plan_args(rope, index)
-    rc = _on_device(index, (_lib or lib()).fa_kv_append, (
+    rc = _on_device(index, lib().fa_kv_append, (
         k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), qp, qop, B, H, Hk, T, d,
         ks, vs, qs, qos, kcs, vcs, P, page, table, blocks, held, new, pp, turns, rot, inter, mag,
         code, _stream_of(index, stream)))
@@ -675,6 +708,10 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, cache_len, o, lse, *, scale: 
     keys and values: writes ``o`` [B,H,T,d] and ``lse`` [B,H,T].  ``tree_mask``: uint8 [T,T] or
     [B,T,T] (row = token, column = new key it sees), None for a chain.  ``workspace``: uint8
     CUDA tensor of ``fa_fwd_paged_workspace_bytes`` bytes.  See include/fa.h."""
+    if _quick is not None and _quick_call(
+            _quick.paged, "fa_fwd_paged", q, k_cache, v_cache, block_table, cache_len, new_len, o,
+            lse, tree_mask, workspace, scale, _handle(stream)):
+        return
     shape, dtype, index, code = _main(q, "q")
     B, H, T, d = shape
     qs = None if q.is_contiguous() else _rows(q, "q", shape, dtype, index)
@@ -690,7 +727,7 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, cache_len, o, lse, *, scale: 
             or workspace.get_device() != index or not workspace.is_contiguous():
         raise FAError(FA_ERR_INVALID_ARG,
                       f"workspace must be a contiguous uint8 tensor on cuda:{index}")
-    rc = _on_device(index, (_lib or lib()).fa_fwd_paged, (
+    rc = _on_device(index, lib().fa_fwd_paged, (
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), lp, B, H, Hk, T, d, qs,
         os_, kcs, vcs, P, page, table, blocks, held, new, tp, per_batch, float(scale), code,
         workspace.data_ptr(), workspace.numel(), _stream_of(index, stream)))

@@ -438,3 +438,69 @@ def test_prompt_then_decode_agrees_with_dense_attention():
         tol = 4 * R.half_step(BF) * float(v.abs().max())
         assert (oo.float() - o[:, :, lo:hi].float()).abs().max() <= tol
         assert (ll - lse[:, :, lo:hi]).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("quick", [True, False], ids=["quick", "ctypes"])
+def test_both_bindings_make_the_same_call(quick, monkeypatch):
+    """The compiled binding and ctypes: strided and contiguous tensors, every optional argument."""
+    assert fa._quick is not None
+    if not quick:
+        monkeypatch.setattr(fa, "_quick", None)
+    c = problem(2, 2, 2, 5, 64, 16, [40, 300], BF, new=[5, 3], tree=True, seed=20)
+    against_reference(c)
+    g = torch.Generator().manual_seed(21)
+    x = on_gpu(c)
+    fused = torch.randn((2, 5, 8, 64), generator=g).to(BF).to(DEV)
+    q, k, v = fused[:, :, :4].transpose(1, 2), fused[:, :, 4:6].transpose(1, 2), fused[:, :, 6:].transpose(1, 2)
+    plan = fa.rope_plan(32)
+    pos = torch.arange(10, dtype=torch.int32, device=DEV).reshape(2, 5)
+    outs = []
+    for args in ((q, k, v), tuple(t.contiguous() for t in (q, k, v))):
+        kc, vc, qo = x["kc"].clone(), x["vc"].clone(), torch.zeros((2, 4, 5, 64), dtype=BF, device=DEV)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        fa.fa_kv_append(args[1], args[2], kc, vc, x["table"], x["cache_len"], new_len=x["new_len"],
+                        rope=plan, positions=pos, q=args[0], q_out=qo, stream=side)
+        side.synchronize()
+        outs.append((qo, kc, vc))
+    for a, b in zip(*outs):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    got = fa.rope(q, plan, k=k, positions=pos[0])
+    want = fa.rope(q.contiguous(), plan, k=k.contiguous(), positions=pos[:1].expand(2, 5).contiguous())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def wrong_calls():
+    z = lambda *s, dtype=FP: torch.zeros(s, dtype=dtype, device=DEV)  # noqa: E731
+    q, kc, lens = z(2, 4, 3, 64), z(9, 2, 16, 64), z(2, dtype=torch.int32)
+    table, lse, ws = z(2, 4, dtype=torch.int32), z(2, 4, 3, dtype=torch.float32), z(1 << 22, dtype=torch.uint8)
+    k, plan = z(2, 2, 3, 64), fa.rope_plan(32)
+    paged = dict(q=q, k_cache=kc, v_cache=kc, block_table=table, cache_len=lens, o=z(2, 4, 3, 64), lse=lse,
+                 scale=0.125, workspace=ws)
+    for over in (dict(q=q.float()), dict(q=q.cpu()), dict(k_cache=kc.bfloat16()), dict(v_cache=kc[:8]),
+                 dict(k_cache=z(9, 3, 16, 64), v_cache=z(9, 3, 16, 64)), dict(block_table=table.long()),
+                 dict(block_table=table[:1]), dict(cache_len=lens[:1]), dict(new_len=lens.cpu()),
+                 dict(o=z(2, 4, 2, 64)), dict(lse=lse.half()), dict(tree_mask=z(3, 4, dtype=torch.uint8)),
+                 dict(tree_mask=z(3, 3)), dict(scale=0.0), dict(scale=float("nan")), dict(workspace=ws[:64]),
+                 dict(workspace=ws.view(torch.int8)), dict(q=q.transpose(2, 3).contiguous().transpose(2, 3)),
+                 dict(o=z(1, 4, 3, 64).expand(2, 4, 3, 64)), dict(k_cache=z(9, 2, 12, 64), v_cache=z(9, 2, 12, 64))):
+        yield "fa_fwd_paged", {**paged, **over}
+    app = dict(k=k, v=k, k_cache=kc, v_cache=kc.clone(), block_table=table, cache_len=lens, rope=plan, q=q, q_out=z(2, 4, 3, 64))
+    for over in (dict(k=k[:, :1]), dict(v=k.bfloat16()), dict(q=None), dict(q_out=None), dict(q=z(2, 4, 2, 64)),
+                 dict(positions=lens), dict(rope=object()), dict(new_len=table), dict(q_out=q[..., :32])):
+        yield "fa_kv_append", {**app, **over}
+    rot = dict(q=q, q_out=z(2, 4, 3, 64), plan=plan, k=k, k_out=z(2, 2, 3, 64))
+    for over in (dict(q_out=z(2, 4, 3, 32)), dict(k_out=None), dict(k=None), dict(k=z(1, 2, 3, 64)),
+                 dict(positions=table), dict(plan=None), dict(q=q.double()), dict(plan=fa.rope_plan(128))):
+        yield "fa_rope", {**rot, **over}
+
+
+@pytest.mark.parametrize("quick", [True, False], ids=["quick", "ctypes"])
+def test_wrong_arguments_are_refused(quick, monkeypatch):
+    if not quick:
+        monkeypatch.setattr(fa, "_quick", None)
+    for name, kw in wrong_calls():
+        with pytest.raises(fa.FAError):
+            getattr(fa, name)(**kw)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK
