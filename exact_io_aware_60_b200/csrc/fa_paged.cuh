@@ -94,12 +94,13 @@ struct PagedCfg {
     // P over S; see the kernel for this form's.)
     static constexpr int SPT = RT;              // steps of a tile
     static constexpr int STEP = BN / SPT;       // keys of a step
-    static constexpr int NSB = (RT == 1) ? 2 : 1;  // score buffers of a row tile
-    // TMEM columns: scores, two buffers of P, O
-    static constexpr uint32_t S_TILE = (RT == 1) ? 0 : 128;  // between row tiles
-    static constexpr uint32_t COL_P = (RT == 1) ? 256 : 64;
+    static constexpr int NSB = (RT == 1 || D == 64) ? 2 : 1;  // score buffers of a row tile
+    // TMEM columns of a row tile: scores, two buffers of P; then O of both
+    static constexpr uint32_t S_BUF = STEP;
+    static constexpr uint32_t COL_P = NSB * STEP;
+    static constexpr uint32_t S_TILE = NSB * STEP + STEP;
     static constexpr uint32_t P_BUF = STEP / 2;
-    static constexpr uint32_t COL_O = (RT == 1) ? 384 : 256;
+    static constexpr uint32_t COL_O = RT * S_TILE;
     static_assert(COL_O + RT * D <= 512, "TMEM budget");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -111,7 +112,7 @@ struct PagedBars {
     // warp waits for is unambiguous.  (Four in turn: S runs at most four tiles ahead of a
     // repair, as P V of the first waits for it.)
     uint64_t need[4];
-    uint64_t s_full[2], s_empty[2];   // index: score buffer (RT = 1) or row tile
+    uint64_t s_full[4], s_empty[4];   // index: NSB * row tile + score buffer
     uint64_t p_full[4], pv_done[4];   // index: 2 * row tile + buffer of P
     // Fills are announced per tile (mod 8; a ring holds at most 6), slots released per slot.
     // fixed: V repaired.
@@ -418,7 +419,8 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 
     // Step n, row tile i: score buffer's barrier and phase, P buffer's barrier and phase.
     constexpr int NSB = C::NSB;
-    auto sb_of = [](int n, int i) { return NSB == 2 ? (n & 1) : i; };
+    auto sb_of = [](int n, int i) { return NSB == 2 ? 2 * i + (n & 1) : i; };
+    auto sb_at = [](int n, int i) { return i * C::S_TILE + (NSB == 2 ? (n & 1) * C::S_BUF : 0u); };
     auto sb_ph = [](int n) { return NSB == 2 ? (n >> 1) & 1 : n & 1; };
     auto pb_of = [](int n, int i) { return 2 * i + (n & 1); };
     auto pb_ph = [](int n) { return (n >> 1) & 1; };
@@ -435,7 +437,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             mbar_init(&bars->mask_full[i], 1);
             mbar_init(&bars->mask_empty[i], C::SOFT);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NSB * RT; ++i) {
             mbar_init(&bars->s_full[i], 1);
             mbar_init(&bars->s_empty[i], 128);
         }
@@ -557,7 +559,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint64_t qo = (uint64_t)(((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4);
                             const uint64_t ko = (uint64_t)(((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4);
-                            mma_ss(tmem + b * 128, qd + qo, kd + ko, kIdesc, kk > 0);
+                            mma_ss(tmem + sb_at(n, i), qd + qo, kd + ko, kIdesc, kk > 0);
                         }
                         // (the barriers that nobody waits for at the end come first, so that no
                         // arrival is outstanding when the CTA ends)
@@ -751,7 +753,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 const int n = n0 + i, b = sb_of(n, ti);
                 const int kt = i % SPT * C::STEP + kw * CW;        // this thread's keys of the tile
                 const int k0 = (it.j0 + i / SPT) * 128 + kt;
-                const uint32_t sb = tmem + lane_base + b * 128 + kw * CW;
+                const uint32_t sb = tmem + lane_base + sb_at(n, ti) + kw * CW;
                 const bool masked = k0 + CW > open;
                 if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[b], sb_ph(n)))) {
                     ok = false;
