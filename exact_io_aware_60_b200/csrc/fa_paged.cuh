@@ -399,6 +399,44 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+// Adds the values that are not finite, columns col .. col + n - 1, of the new keys that token
+// tk sees among the piece's to v.  (Out of line, as is the next: rare, and the code that every
+// piece runs through comes in from memory at each launch.)
+template <bool BF16>
+__device__ __noinline__ void paged_add_not_finite(const PagedParams &p, const PagedSeg &it, float *v, int n,
+                                                  int col, int tk) {
+    for (int j = max(it.past, it.j0 * 128); j < min(it.total, it.j1 * 128); ++j) {
+        const int x = j - it.past;
+        const bool seen = p.tree ? p.tree[it.b * p.tree_sb + (long long)tk * p.T + x] != 0 : x <= tk;
+        const int id = p.pt.table[(long long)it.b * p.pt.max_blocks + (j >> p.pt.page_shift)];
+        if (!seen || id < 0 || id >= p.pt.num_pages) continue;
+        const uint16_t *src = p.vc.p + id * p.vc.sb + it.hk * p.vc.sh +
+                              (j & ((1 << p.pt.page_shift) - 1)) * p.vc.st + col;
+        for (int e = 0; e < n; ++e) {
+            const uint32_t w = src[e];
+            if (not_finite2<BF16>(w) & 0xffffu) v[e] += unpack2<BF16>(w).x;
+        }
+    }
+}
+
+// New keys x0 .. x0 + 31 (x0 > -32) that token tok sees, from a mask of more than 128 columns.
+__device__ __noinline__ uint32_t paged_tree_bits(const PagedParams &p, int b, int fresh, int tok, int x0) {
+    uint32_t bits = x0 >= 0 ? 0u : (1u << -x0) - 1u;
+    const uint8_t *mr = p.tree + b * p.tree_sb + (long long)tok * p.T + x0;
+    const int lo = max(0, -x0), hi = min(32, fresh - x0);
+    for (int c = lo; c < hi; ++c) bits |= (__ldg(mr + c) != 0 ? 1u : 0u) << c;
+    return bits;
+}
+
+// Keys of 32 from place kt of a tile on whose pages lie outside the cache.
+__device__ __noinline__ uint32_t paged_bad_bits(uint32_t bad, int page_shift, int kt) {
+    const int sh = min(page_shift, 7), sub = min(1 << sh, 32);
+    uint32_t bits = 0u;
+    for (int c = 0; c < 32; c += sub)
+        if ((bad >> ((kt + c) >> sh)) & 1u) bits |= (sub == 32 ? 0xffffffffu : (1u << sub) - 1u) << c;
+    return bits;
+}
+
 template <int D, bool BF16, int REP, int RT>
 __global__ void __launch_bounds__(PagedCfg<D, REP, RT>::THREADS, 1)
 fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -778,17 +816,10 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         const uint32_t hi = q + 1 < 0 ? 0xffffffffu : (q + 1 < nw ? mr[q + 1] : 0u);
                         bits = __funnelshift_r(lo, hi, x0 & 31);
                     } else {
-                        bits = x0 >= 0 ? 0u : (x0 <= -32 ? 0xffffffffu : (1u << -x0) - 1u);
-                        const uint8_t *mr = p.tree + it.b * p.tree_sb + (long long)tok * p.T + x0;
-                        const int lo = max(0, -x0), hi = min(32, it.fresh - x0);
-                        for (int c = lo; c < hi; ++c) bits |= (__ldg(mr + c) != 0 ? 1u : 0u) << c;
+                        bits = x0 <= -32 ? 0xffffffffu : paged_tree_bits(p, it.b, it.fresh, tok, x0);
                     }
-                    if (bad) {  // keys of pages outside the cache are not visible
-                        const int sh = min(p.pt.page_shift, 7), sub = min(1 << sh, 32);
-                        for (int c = 0; c < 32; c += sub)
-                            if ((bad >> ((kt + w * 32 + c) >> sh)) & 1u)
-                                bits &= ~((sub == 32 ? 0xffffffffu : (1u << sub) - 1u) << c);
-                    }
+                    // keys of pages outside the cache are not visible
+                    if (bad) bits &= ~paged_bad_bits(bad, p.pt.page_shift, kt + w * 32);
                     return bits;
                 };
                 // The maximum.  Up to 64 scores stay in registers; 128 are read from TMEM in two
@@ -925,21 +956,6 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             // Values that the repair cleared reach the rows that do see them (rare: only where
             // a new key's V is not finite, and slow).
             const bool poison = nt > 0 && it.repair(p, it.j1 - 1) && bars->poison[t & 3] != 0;
-            auto add_not_finite = [&](float *v, int n, int col, int tk) {
-                for (int j = max(it.past, it.j0 * 128); j < min(it.total, it.j1 * 128); ++j) {
-                    const int x = j - it.past;
-                    const bool seen = p.tree ? p.tree[it.b * p.tree_sb + (long long)tk * p.T + x] != 0
-                                             : x <= tk;
-                    const int id = p.pt.table[(long long)it.b * p.pt.max_blocks + (j >> p.pt.page_shift)];
-                    if (!seen || id < 0 || id >= p.pt.num_pages) continue;
-                    const uint16_t *src = p.vc.p + id * p.vc.sb + it.hk * p.vc.sh +
-                                          (j & ((1 << p.pt.page_shift) - 1)) * p.vc.st + col;
-                    for (int e = 0; e < n; ++e) {
-                        const uint32_t w = src[e];
-                        if (not_finite2<BF16>(w) & 0xffffu) v[e] += unpack2<BF16>(w).x;
-                    }
-                }
-            };
             auto out_row = [&](int h, int tk) {
                 return const_cast<uint16_t *>(p.o.p) + it.b * p.o.sb + (it.hk * p.G + h) * p.o.sh + tk * p.o.st;
             };
@@ -961,7 +977,14 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         tc_fence_before();
                         mbar_arrive(&bars->o_empty);
                     }
-                    if (poison && live) add_not_finite(v, 32, c32 * 32, tok);
+                    if (poison && live) {  // (a copy: v itself stays in registers)
+                        float x[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = v[e];
+                        paged_add_not_finite<BF16>(p, it, x, 32, c32 * 32, tok);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = x[e];
+                    }
                     if (it.whole) {
                         // through shared memory, so that a store covers 64 bytes of 8 rows
                         // instead of 16 bytes of 32 (16-byte chunks permuted by row pairs)
@@ -1077,7 +1100,11 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                                 v[3] += y.w;
                             }
                         }
-                        if (poison && dtok[e] < it.fresh) add_not_finite(v, 4, c0 + c4, dtok[e]);
+                        if (poison && dtok[e] < it.fresh) {
+                            float y[4] = {v[0], v[1], v[2], v[3]};
+                            paged_add_not_finite<BF16>(p, it, y, 4, c0 + c4, dtok[e]);
+                            v[0] = y[0], v[1] = y[1], v[2] = y[2], v[3] = y[3];
+                        }
                         if (it.whole)
                             *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst[e]) + c0) =
                                 make_uint2(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]));
