@@ -389,7 +389,8 @@ FA_API int fa_kv_append(const void *k, const void *v, void *k_cache, void *v_cac
  *     j < cache_len[b], or  i = j - cache_len[b] < new_len[b]  and
  *     (tree_mask ? tree_mask[b][t][i] != 0 : i <= t),
  * so one token, a chain (a prompt's chunk) or a tree of drafted tokens are the same call.
- *   q, o        : DEVICE [B, H, T, d] 16-bit; *_strides as fa_rope (o not a broadcast).
+ *   q, o        : DEVICE [B, H, T, d] 16-bit, not overlapping; *_strides as fa_rope, neither a
+ *                 broadcast.
  *   lse         : DEVICE [B, H, T] fp32, contiguous.
  *   k_cache .. new_len : as fa_kv_append (read only).
  *   tree_mask   : DEVICE uint8 [T, T] (tree_per_batch = 0) or [B, T, T] (1), row = token,

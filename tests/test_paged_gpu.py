@@ -89,6 +89,12 @@ CASES = [
     (40, 2, 2, 1, 64, 16, [(37 * i) % 300 for i in range(40)], FP, None, False),  # many short
     (1, 1, 4, 1, 128, 64, [20000], BF, None, False),       # one long: cut into many pieces
     (1, 1, 1, 64, 64, 32, [9000], FP, None, True),
+    (2, 2, 5, 20, 128, 32, [90, 256], FP, [20, 11], True), # one row tile, not repeated
+    (1, 1, 1, 129, 64, 16, [77], BF, None, True),          # masks of more than 128 columns
+    (2, 1, 2, 200, 128, 32, [0, 500], FP, [200, 170], True),
+    (1, 1, 130, 2, 64, 16, [140], BF, None, True),         # a token's heads in two row tiles
+    (2, 1, 300, 1, 128, 64, [10, 200], FP, None, False),
+    (1, 2, 128, 3, 64, 32, [50], FP, None, False),
 ]
 
 
@@ -144,7 +150,7 @@ def test_new_rows_behind_the_last_are_empty():
 
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
-@pytest.mark.parametrize("T,G", [(12, 2), (12, 5), (50, 4)])
+@pytest.mark.parametrize("T,G", [(12, 2), (12, 5), (20, 5), (50, 4)])
 def test_not_finite_values_in_hidden_keys(value, T, G):
     """A drafted token's K and V that are not finite reach the rows that see it, and no other."""
     c = problem(1, 1, G, T, 64, 16, [100], FP, tree=True, seed=6)

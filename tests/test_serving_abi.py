@@ -152,3 +152,17 @@ def test_binding_refuses_cpu_tensors():
     with pytest.raises(fa.FAError):
         fa.fa_fwd_paged(x, x, x, i[None], i, x, x[..., 0].float(), scale=1.0,
                         workspace=torch.zeros(8, dtype=torch.uint8))
+
+
+def test_quick_binding_leaves_other_calls_alone():
+    """What is not a plain call gets None, with nothing called (the address is null)."""
+    assert fa._quick is not None
+    x = torch.zeros((1, 2, 4, 64), dtype=torch.float16)
+    i = torch.zeros(1, dtype=torch.int32)
+    turns = torch.zeros(32, dtype=torch.int64)
+    assert fa._quick.rope(0, x, x, None, None, None, turns, 64, False, 1.0, None) is None
+    assert fa._quick.rope(0, None, x, None, None, None, turns, 64, False, 1.0, None) is None
+    assert fa._quick.rope(0) is None
+    assert fa._quick.append(0, x, x, x, x, i[None], i, None, None, None, None, None, 0, False, 1.0,
+                            None) is None
+    assert fa._quick.paged(0, x, x, x, i[None], i, None, x, x, None, x, "scale", None) is None
