@@ -873,12 +873,11 @@ int launch_paged(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap
     }
     e = launch_pdl(kern, dim3((unsigned)p.ctas), dim3(C::THREADS), C::SMEM, st, mq, mk, mv, p);
     if (e == cudaSuccess && !p.uncut) {
-        constexpr bool TRANS = REP == 1;
-        // rows in use: all of an item's, or those of the call's tokens where these are fewer
+        // groups of 32 rows in use: all of an item's, or those of the call's tokens where these
+        // are fewer (one block for up to 64 rows)
         const int rows = RT == 2 ? 256 : std::min(p.TPT, p.T) * p.GP;
-        e = launch_pdl(fa::fa_paged_merge_kernel<D, BF16, RT, TRANS>,
-                       dim3((unsigned)p.ctas, (unsigned)((rows + 31) / 32)), dim3(256), 0, st, p,
-                       (int)C::ROWS);
+        e = launch_pdl(fa::fa_paged_merge_kernel<D, BF16, REP, RT>,
+                       dim3((unsigned)p.ctas, REP > 1 ? 1u : (unsigned)((rows + 31) / 32)), dim3(256), 0, st, p);
     }
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {

@@ -1137,11 +1137,15 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 // A share leaves at most one item unfinished that it began: grid.x = shares.  The item, its
 // pieces and their places are worked out before the wait for the attention kernel (which
 // triggers this launch behind its own wait, so that the lengths are final by then).
-// TRANS (rows of a piece as [column / 4][row]): grid.y = groups of 32 rows, a lane is a row, a
-// warp 1 / 8 of the columns.  Else: a warp is a row at a time, a lane 1 / 32 of the columns.
-template <int D, bool BF16, int RT, bool TRANS>
-__global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_constant__ PagedParams p,
-                                                             const int rows) {
+// Without copies (TRANS, rows of a piece as [column / 4][row]): grid.y = groups of 32 rows, a
+// lane is a row, a warp 1 / 8 of the columns.  With copies a block takes all rows, so that the
+// whole grid is in place beside the attention kernel's when that ends: a warp is a row at a
+// time, a lane 1 / 32 of the columns.
+// (64 registers: what the attention kernel leaves of an SM's is 17000)
+template <int D, bool BF16, int REP, int RT>
+__global__ void __launch_bounds__(256, 4) fa_paged_merge_kernel(const __grid_constant__ PagedParams p) {
+    constexpr bool TRANS = REP == 1;
+    constexpr int ROWS = 128 / REP;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c0 = blockIdx.x;
     pdl_launch_dependents();  // (whoever comes next waits for this grid's end in its turn)
@@ -1166,79 +1170,107 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
     }
     pdl_wait();
     if (!cut) return;
-    // Each round takes four pieces, log-sum-exps and outputs together, into a running maximum
-    // and sum: one wait on L2 (about 0.7 us) a round.
-    constexpr int NR = TRANS ? 1 : 4;          // rows of a thread in a group of 32
-    constexpr int E = TRANS ? D / 8 : D / 32;  // columns of a thread
-    constexpr int U = 4;
-#pragma unroll 2
-    for (int k = 0; k < NR; ++k) {
-        const int row = blockIdx.y * 32 + (TRANS ? lane : k * 8 + warp);  // of the item
-        const int tile = row / rows, r = row - tile * rows;
-        const int tl = r * p.gp_magic >> 16, tt = rt / p.GT;
-        const int tok = (tt * RT + tile) * p.TPT + tl, head = (rt - tt * p.GT) * p.GP + (r - tl * p.GP);
-        if (tile >= RT || tl >= p.TPT || tok >= p.T || head >= p.G) continue;
-        float acc[E], sum = 0.f, M = -INFINITY;
+    // Each round takes U pieces of R rows, log-sum-exps and outputs together, into a running
+    // maximum and sum: one wait on L2 (about 0.7 us) a round.  Few rows come in many pieces
+    // (decoding), many rows in few.
+    constexpr int E = TRANS ? D / 8 : D / 32;             // columns of a thread
+    constexpr int R = TRANS ? 1 : (REP == 4 ? 1 : 2), U = TRANS ? 4 : (REP == 4 ? 8 : 3);
+    constexpr int NR = TRANS ? 1 : (REP == 4 ? 4 : 8);    // rows of a thread
+#pragma unroll 1
+    for (int k = 0; k < NR; k += R) {
+        int row[R], tok[R], head[R];
+        bool in[R], any = false;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        for (int j = 0; j < R; ++j) {
+            row[j] = TRANS ? blockIdx.y * 32 + lane : (k + j) * 8 + warp;  // of the item
+            const int tile = row[j] / ROWS, r = row[j] - tile * ROWS;
+            const int tl = r * p.gp_magic >> 16, tt = rt / p.GT;
+            tok[j] = (tt * RT + tile) * p.TPT + tl;
+            head[j] = (rt - tt * p.GT) * p.GP + (r - tl * p.GP);
+            in[j] = tile < RT && tl < p.TPT && tok[j] < p.T && head[j] < p.G;
+            any = any || in[j];
+            if (!in[j]) row[j] = 0;
+        }
+        if (!any) continue;
+        float acc[R][E], sum[R], M[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            sum[j] = 0.f;
+            M[j] = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[j][e] = 0.f;
+        }
         for (int s0 = c0; s0 <= c1; s0 += U) {
-            float ls[U], v[U][E];
+            float ls[U][R], v[U][R][E];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int c = min(s0 + u, c1);
-                const long long at = (2LL * c + (c == c0 ? first : 0)) * (RT * rows);
-                ls[u] = s0 + u <= c1 ? p.part_lse[at + row] : -INFINITY;
-                if constexpr (TRANS) {
-                    const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (at + tile * rows) * D) +
-                                        warp * (E / 4) * rows + r;
+                const long long at = (2LL * c + (c == c0 ? first : 0)) * (RT * ROWS);
 #pragma unroll
-                    for (int e = 0; e < E / 4; ++e) {
-                        const float4 x = src[e * rows];
-                        v[u][4 * e] = x.x, v[u][4 * e + 1] = x.y, v[u][4 * e + 2] = x.z, v[u][4 * e + 3] = x.w;
+                for (int j = 0; j < R; ++j) {
+                    ls[u][j] = s0 + u <= c1 ? p.part_lse[at + row[j]] : -INFINITY;
+                    if constexpr (TRANS) {
+                        const int tile = row[j] / ROWS, r = row[j] - tile * ROWS;
+                        const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (at + tile * ROWS) * D) +
+                                            warp * (E / 4) * ROWS + r;
+#pragma unroll
+                        for (int e = 0; e < E / 4; ++e) {
+                            const float4 x = src[e * ROWS];
+                            v[u][j][4 * e] = x.x, v[u][j][4 * e + 1] = x.y;
+                            v[u][j][4 * e + 2] = x.z, v[u][j][4 * e + 3] = x.w;
+                        }
+                    } else if constexpr (E == 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(p.part_o + (at + row[j]) * D + lane * E);
+                        v[u][j][0] = x.x, v[u][j][1] = x.y, v[u][j][2] = x.z, v[u][j][3] = x.w;
+                    } else {
+                        const float2 x = *reinterpret_cast<const float2 *>(p.part_o + (at + row[j]) * D + lane * E);
+                        v[u][j][0] = x.x, v[u][j][1] = x.y;
                     }
-                } else if constexpr (E == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(p.part_o + (at + row) * D + lane * E);
-                    v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
-                } else {
-                    const float2 x = *reinterpret_cast<const float2 *>(p.part_o + (at + row) * D + lane * E);
-                    v[u][0] = x.x, v[u][1] = x.y;
                 }
             }
-            float M1 = M;
 #pragma unroll
-            for (int u = 0; u < U; ++u) M1 = fmaxf(M1, ls[u]);
-            const float alpha = M == -INFINITY ? 0.f : ex2(M - M1);
-            M = M1;
-            sum *= alpha;
+            for (int j = 0; j < R; ++j) {
+                float M1 = M[j];
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] *= alpha;
+                for (int u = 0; u < U; ++u) M1 = fmaxf(M1, ls[u][j]);
+                const float alpha = M[j] == -INFINITY ? 0.f : ex2(M[j] - M1);
+                M[j] = M1;
+                sum[j] *= alpha;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float w = ls[u] == -INFINITY ? 0.f : ex2(ls[u] - M1);  // (NaN is carried on)
-                sum += w;
+                for (int e = 0; e < E; ++e) acc[j][e] *= alpha;
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[u][e], acc[e]);
+                for (int u = 0; u < U; ++u) {
+                    const float w = ls[u][j] == -INFINITY ? 0.f : ex2(ls[u][j] - M1);  // (NaN is carried on)
+                    sum[j] += w;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[j][e] = fmaf(w, v[u][j][e], acc[j][e]);
+                }
             }
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int h = hk * p.G + head;
-        uint32_t *o = reinterpret_cast<uint32_t *>(const_cast<uint16_t *>(p.o.p) + b * p.o.sb + h * p.o.sh +
-                                                   tok * p.o.st + (TRANS ? warp : lane) * E);
-        uint32_t w[E / 2];
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) w[e] = sum == 0.f ? 0u : pack2<BF16>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-        if constexpr (E / 2 >= 4) {
+        for (int j = 0; j < R; ++j) {
+            if (!in[j]) continue;
+            const float inv = sum[j] == 0.f ? 0.f : 1.f / sum[j];
+            const int h = hk * p.G + head[j];
+            uint32_t *o = reinterpret_cast<uint32_t *>(const_cast<uint16_t *>(p.o.p) + b * p.o.sb + h * p.o.sh +
+                                                       tok[j] * p.o.st + (TRANS ? warp : lane) * E);
+            uint32_t w[E / 2];
 #pragma unroll
-            for (int e = 0; e < E / 8; ++e)
-                reinterpret_cast<uint4 *>(o)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-        } else if constexpr (E / 2 == 2) {
-            *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
-        } else {
-            *o = w[0];
+            for (int e = 0; e < E / 2; ++e)
+                w[e] = sum[j] == 0.f ? 0u : pack2<BF16>(acc[j][2 * e] * inv, acc[j][2 * e + 1] * inv);
+            if constexpr (E / 2 >= 4) {
+#pragma unroll
+                for (int e = 0; e < E / 8; ++e)
+                    reinterpret_cast<uint4 *>(o)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            } else if constexpr (E / 2 == 2) {
+                *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+            } else {
+                *o = w[0];
+            }
+            if (TRANS ? warp == 0 : lane == 0)
+                p.lse[((long long)b * p.Hk * p.G + h) * p.T + tok[j]] =
+                    sum[j] == 0.f ? -INFINITY : (M[j] + lg2(sum[j])) * 0.69314718055994531f;
         }
-        if (TRANS ? warp == 0 : lane == 0)
-            p.lse[((long long)b * p.Hk * p.G + h) * p.T + tok] =
-                sum == 0.f ? -INFINITY : (M + lg2(sum)) * 0.69314718055994531f;
     }
 }
 
