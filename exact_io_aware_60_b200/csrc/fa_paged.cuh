@@ -22,7 +22,7 @@
 // cut item go to the workspace as fp32 (normalised O, log-sum-exp) and a second kernel,
 // launched early by PDL, merges them in a fixed order.
 //
-// CTA: softmax warps (one row per thread, 4 per row tile), then one producer warp (page table
+// CTA: softmax warps (one row per thread, 4 per row tile), then one or two loaders (page table
 // and TMA of K and V), one issuer of S, one of P V, and one that works out the CTA's pieces of
 // work two ahead of the others (its lookups of lengths, about 1 us an item, are off everybody's
 // path), loads Q and repairs V tiles (see repair).  Two issuers, because a commit leaves the
