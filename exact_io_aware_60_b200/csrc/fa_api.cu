@@ -1342,8 +1342,13 @@ int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *
     p.gp_magic = (65536u + sh.GP - 1) / sh.GP;
     p.GT = sh.GT;
     p.TPT = sh.TPT;
-    // Up to four tiles an item are not cut: a tile more takes about 1 us, the merge 3 us.
-    p.uncut = cap_tiles <= 4;
+    // Short items are not cut: with up to 64 rows a tile more takes 0.5 us (d = 64; 0.6 at 128),
+    // without copies of the rows 1.1 to 2 us, against 4 to 5 us for the merge and the pieces.
+    // Measured, cut and not (one token, 4 rows, d = 64): 2 items of 5 tiles 8.5 and 7.9 us, of 8
+    // tiles 8.6 and 9.8; 32 items of 8 tiles 11.2 and 10.2; 256 items of 10 tiles 28.1 and 23.1;
+    // 80 rows, 16 items of 4 tiles 12.9 and 12.6 (d = 128), of 5 tiles 11.6 and 12.8 (d = 64).
+    const long long items = sh.row_tiles * Hk * B;
+    p.uncut = cap_tiles <= (sh.rows > 64 ? 4 : items < 32 ? 6 : 10);
     p.row_tiles = (int)sh.row_tiles;
     p.ctas = (int)std::min<double>(ctas, (double)sh.row_tiles * Hk * B * cap_tiles);
     p.scale_log2 = scale * 1.4426950408889634f;

@@ -148,7 +148,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams &p, int b) {
     page_lengths(p.pt, p.T, b, s.past, s.fresh);
     s.tiles = (s.past + s.fresh + 127) >> 7;
     s.valid = (s.fresh + p.TPT * RT - 1) / (p.TPT * RT) * p.GT;
-    s.per_head = p.uncut ? p.row_tiles : s.valid * (s.tiles + kItemCost) + (p.row_tiles - s.valid);
+    s.per_head = s.valid * (s.tiles + kItemCost) + (p.row_tiles - s.valid);
     return s;
 }
 
@@ -231,18 +231,21 @@ struct PagedWalk {
     }
     // Share c of all units; returns the shares.
     __device__ __forceinline__ PagedShares init(const PagedParams &p, int c, int lane) {
-        int W = 0;
-        for (int k = 0; k < p.B; k += 32) {
-            load(p, k, lane);
-            W += warp_sum(mine);
+        int W = p.B * p.Hk * p.row_tiles;  // uncut: a unit is an item, no length is needed
+        if (!p.uncut) {
+            W = 0;
+            for (int k = 0; k < p.B; k += 32) {
+                load(p, k, lane);
+                W += warp_sum(mine);
+            }
+            if (p.B > 32) load(p, 0, lane);
+            base = 0;
+            upto = warp_scan(mine, lane);
         }
         PagedShares sh;
         sh.init(W, p.ctas);
         u = min(sh.begin(c), W);
         u1 = min(sh.begin(c + 1), W);
-        if (p.B > 32) load(p, 0, lane);
-        base = 0;
-        upto = warp_scan(mine, lane);
         n = 0;
         first = true;
         done = false;
@@ -253,6 +256,12 @@ struct PagedWalk {
         int b, hk, r, past, fresh, tiles, valid;
     };
     __device__ __forceinline__ Place place(const PagedParams &p, int lane) {
+        if (p.uncut) {
+            const int per = p.Hk * p.row_tiles, b = (unsigned)u / (unsigned)per, r0 = u - b * per;
+            const int hk = (unsigned)r0 / (unsigned)p.row_tiles;
+            const PagedSeq s = paged_seq<RT>(p, b);
+            return Place{b, hk, r0 - hk * p.row_tiles, s.past, s.fresh, s.tiles, s.valid};
+        }
         for (int all; base + (all = __shfl_sync(0xffffffffu, upto, 31)) <= u;) {
             base += all;
             load(p, k0 + 32, lane);
