@@ -510,3 +510,49 @@ def test_wrong_arguments_are_refused(quick, monkeypatch):
             getattr(fa, name)(**kw)
     torch.cuda.synchronize()
     assert fa.fa_get_device_status() == fa.FA_OK
+
+
+def test_two_host_threads():
+    """Calls of two host threads at once, each on its own stream with its own workspace."""
+    import threading
+
+    cs = [problem(2, 2, 4, 3, 128, 32, [2000, 60], BF, tree=True, seed=30),
+          problem(1, 2, 2, 150, 64, 64, [700], FP, seed=31)]
+    want = [run(c) for c in cs]
+    xs = [on_gpu(c) for c in cs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        st, x = torch.cuda.Stream(), xs[i]
+        for _ in range(20):
+            o, lse = fa.forward_paged(x["q"], x["kc"], x["vc"], x["table"], x["cache_len"],
+                                      tree_mask=x["tree"], stream=st)
+            st.synchronize()
+            if not (torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and fa.fa_get_device_status() == fa.FA_OK
+
+
+def test_many_rows_captured_and_replayed():
+    """A chunk with two row tiles and its merge in a graph, lengths changing between replays."""
+    c = problem(2, 2, 2, 180, 128, 64, [3000, 400], BF, seed=32)
+    x = on_gpu(c)
+    o, lse = torch.empty_like(x["q"]), torch.empty(x["q"].shape[:3], device=DEV)
+    ws = fa.paged_workspace_for(x["q"], 2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fa.fa_fwd_paged(x["q"], x["kc"], x["vc"], x["table"], x["cache_len"], o, lse,
+                        scale=128 ** -0.5, workspace=ws)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run(dict(c, cache_len=x["cache_len"].cpu()))
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        x["cache_len"].sub_(130)
