@@ -33,6 +33,10 @@
 // REP lane quarters / halves, and each copy takes 1 / REP of the keys of every tile as a
 // softmax of its own (P is zero elsewhere); the copies are merged in the epilogue.  The
 // exponentials of a tile then take 1 / REP of the time.
+// At d = 64, where a tile's bytes take less than its 128 exponentials a row, one row tile has
+// two groups of softmax warps (KS = 2) that take the key tiles in turn, each with an O of its
+// own, merged in the epilogue (16 sequences of 4000 keys, 32 new tokens, 32 heads over 8: 55 us
+// with one group, 47 with two; a single tile costs 0.3 us more).
 // Many rows (RT = 2): two tiles of 128 rows share every K and V tile, each with softmax warps
 // of its own, so that one tile's products run beside the other's exponentials.
 #pragma once
@@ -69,6 +73,7 @@ struct PagedCfg {
     static_assert(REP == 1 || RT == 1, "copies of one row tile, or two row tiles");
     static constexpr int BN = 128;              // keys per tile
     static constexpr int ROWS = 128 / REP;      // rows of a row tile
+    static constexpr int KS = (D == 64 && REP == 1 && RT == 1) ? 2 : 1;  // softmax groups of a row tile
     static constexpr int HALVES = D / 64;
     static constexpr int QTILE = 128 * D * 2;
     static constexpr int TILE = BN * D * 2;     // K or V tile
@@ -76,20 +81,20 @@ struct PagedCfg {
     // rings of K and V tiles (V, used later, has the odd slot: 62 -> 56 us for decoding 32K
     // keys at d = 64 from pages of 16)
     static constexpr int NK = (D == 64) ? 5 : 2;
-    static constexpr int NV = (D == 64) ? (RT == 1 ? 6 : 5) : (RT == 1 ? 3 : 2);
+    static constexpr int NV = (D == 64) ? (RT == 1 && KS == 1 ? 6 : 5) : (RT == 1 ? 3 : 2);
     // epilogue: REP > 1, a 32-column block of every row and copy, rows padded to 36 columns;
     // else 32 rows x 32 columns of 16 bits for each warp
-    static constexpr int MERGE = (REP > 1) ? 128 * 36 * 4 : RT * 4 * 2048;
+    static constexpr int MERGE = (REP > 1) ? 128 * 36 * 4 : RT * 4 * 2048 + (KS > 1 ? 128 * 36 * 4 : 0);
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + RT * QTILE;
     static constexpr int OFF_MERGE = OFF_RING + (NK + NV) * TILE;
     static constexpr int OFF_BAR = OFF_MERGE + MERGE;
-    static constexpr int USED = OFF_BAR + 3200 + 8192;
+    static constexpr int USED = OFF_BAR + 4864 + 8192;
     static constexpr int SMEM = USED + 1024;
-    static constexpr int SOFT = 4 * RT;         // softmax warps
+    static constexpr int SOFT = 4 * RT * KS;    // softmax warps
     // K and V come from a warp each where the registers allow one more: a box takes about
     // 45 ns to issue, and pages of 16 tokens are 32 boxes a tile at d = 128.
-    static constexpr int LOADERS = (RT == 1) ? 2 : 1;
+    static constexpr int LOADERS = (SOFT == 4) ? 2 : 1;
     static constexpr int THREADS = 32 * (SOFT + 3 + LOADERS);
     // The softmax goes in steps: whole tiles (RT = 1) or 64 keys (RT = 2), whose scores a
     // thread holds in registers, so that the one score buffer that TMEM has room for at
@@ -105,7 +110,7 @@ struct PagedCfg {
     static constexpr uint32_t S_TILE = NSB * STEP + STEP;
     static constexpr uint32_t P_BUF = STEP / 2;
     static constexpr uint32_t COL_O = RT * S_TILE;
-    static_assert(COL_O + RT * D <= 512, "TMEM budget");
+    static_assert(COL_O + RT * KS * D <= 512, "TMEM budget");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -130,7 +135,7 @@ struct PagedBars {
     // Item t & 3 hides keys whose V is not finite.  (Four: the repairing warp reaches item
     // t + 4 only after the softmax of item t + 1 began.)
     int poison[4];
-    float stat[3][128];     // REP merge: m, l, l of the rounded weights
+    float stat[3][256];     // merge of copies or groups: m, l, l of the rounded weights
     uint32_t mask[2][1024]; // per token of the piece, up to 128 bits: the new keys it sees
 };
 
@@ -457,14 +462,14 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     using C = PagedCfg<D, REP, RT>;
     constexpr int ROWS = C::ROWS;
     constexpr int CW = C::STEP / REP; // keys of a step that one thread handles
-    constexpr int SPT = C::SPT;
+    constexpr int SPT = C::SPT, KS = C::KS;
     constexpr int W_S = C::SOFT, W_PV = C::SOFT + 1, W_FIX = C::SOFT + 2, W_TMA = C::SOFT + 3;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sQ = smem + C::OFF_Q;
     uint8_t *ring = smem + C::OFF_RING;
     PagedBars *bars = reinterpret_cast<PagedBars *>(smem + C::OFF_BAR);
-    static_assert(sizeof(PagedBars) <= 3200 + 8192, "barrier area");
+    static_assert(sizeof(PagedBars) <= 4864 + 8192, "barrier area");
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
@@ -482,7 +487,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         tma_prefetch_desc(&tmV);
         mbar_init(&bars->q_full, 1);
         mbar_init(&bars->q_empty, 1);
-        mbar_init(&bars->o_empty, 128 * RT);
+        mbar_init(&bars->o_empty, 32 * C::SOFT);
         for (int i = 0; i < 4; ++i) mbar_init(&bars->need[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->mask_full[i], 1);
@@ -656,8 +661,8 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         const uint32_t pa = tmem + C::COL_P + i * C::S_TILE + (n & 1) * C::P_BUF;
 #pragma unroll
                         for (int kk = 0; kk < C::STEP / 16; ++kk)
-                            mma_ts(tmem + C::COL_O + i * D, pa + kk * 8,
-                                   vd + (uint64_t)((kk * 16 * 128) >> 4), kIdesc, x > 0 || kk > 0);
+                            mma_ts(tmem + C::COL_O + (KS == 2 ? n & 1 : i) * D, pa + kk * 8,
+                                   vd + (uint64_t)((kk * 16 * 128) >> 4), kIdesc, x >= KS || kk > 0);
                         if (i == RT - 1 && h == SPT - 1) mma_commit(&bars->vempty[g % C::NV]);
                         mma_commit(&bars->pv_done[b]);
                     }
@@ -770,11 +775,12 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // ------------------------------ softmax warps -----------------------------------
         constexpr int WPC = 4 / REP;                       // warps of one copy of the rows
         const int ti = RT == 1 ? 0 : warp >> 2;            // row tile
+        const int ks = KS == 1 ? 0 : warp >> 2;            // group: tiles n with n % KS == ks
         const int wq = warp & 3;                           // lane quarter of TMEM
         const int row = (wq % WPC) * 32 + lane;            // row of the tile
         const int kw = wq / WPC;                           // the copy: keys [kw * CW, + CW)
         const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
-        const uint32_t ob = tmem + lane_base + C::COL_O + ti * D;
+        const uint32_t ob = tmem + lane_base + C::COL_O + (ti + ks) * D;
         const float sl2 = p.scale_log2;
         const int tl = row * p.gp_magic >> 16, gl = row - tl * p.GP;  // the row's token and head
         if constexpr (REP > 1) {  // P is zero outside the copy's own keys
@@ -800,7 +806,9 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             float m = -INFINITY;   // running maximum, base 2
             float l = 0.f;         // running sum
             float lr = 0.f;        // the same sum of the rounded weights
-            for (int i = 0; ok && i < nt * SPT; ++i) {
+            const int i0 = KS == 1 ? 0 : ((n0 ^ ks) & 1);  // the group's first tile of the piece
+            const bool has = i0 < nt * SPT;
+            for (int i = i0; ok && i < nt * SPT; i += KS) {
                 const int n = n0 + i, b = sb_of(n, ti);
                 const int kt = i % SPT * C::STEP + kw * CW;        // this thread's keys of the tile
                 const int k0 = (it.j0 + i / SPT) * 128 + kt;
@@ -884,13 +892,13 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 }
                 const float m_use = (m == -INFINITY) ? 0.f : m;
                 // P's buffer is free once P V of step n - 2 is done; O may be rescaled once that
-                // of step n - 1 is.
+                // of step n - 1 is (two groups: n - 2, the group's last).
                 if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[pb_of(n, ti)], pb_ph(n - 2)))) {
                     ok = false;
                     break;
                 }
-                if (i > 0 && any_grow) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[pb_of(n - 1, ti)], pb_ph(n - 1)))) {
+                if (i >= KS && any_grow) {
+                    if (KS == 1 && !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[pb_of(n - 1, ti)], pb_ph(n - 1)))) {
                         ok = false;
                         break;
                     }
@@ -953,18 +961,20 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 ++masks;
             }
             // ------------------------------ epilogue of the piece ------------------------
-            if (ok && nt > 0) {
-                const int n = n0 + nt * SPT - 1;
+            if (ok && has) {
+                int n = n0 + nt * SPT - 1;
+                if (KS == 2 && (n & 1) != ks) --n;
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[pb_of(n, ti)], pb_ph(n)));
                 tc_fence_after();
             }
             // (the merge of the copies has barriers of all four warps: they leave together)
-            if constexpr (REP > 1)
-                if (nt > 0) ok = named_bar_and(1, 128, ok);
+            if constexpr (REP > 1 || KS > 1)
+                if (nt > 0) ok = named_bar_and(1, 128 * KS, ok);
             if (!ok) break;
             if (!live) m = -INFINITY, l = lr = 0.f;  // rows behind the last new token are empty
             bool none = l == 0.f;                    // (a NaN sum is carried to O and LSE)
-            const float inv = none ? 0.f : 1.f / lr;
+            float inv = none ? 0.f : 1.f / lr;
+            const bool writer = KS == 1 || (nt == 1 ? has : ks == 0);  // (one tile: its group alone)
             float lse2 = none ? -INFINITY : m + lg2(l);
             // Values that the repair cleared reach the rows that do see them (rare: only where
             // a new key's V is not finite, and slow).
@@ -974,10 +984,27 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             };
             const long long prow0 = (long long)it.slot * (RT * ROWS) + ti * ROWS;  // first row of the partial
             if constexpr (REP == 1) {
+                float *other = reinterpret_cast<float *>(smem + C::OFF_MERGE + 4 * 2048) + row * 36;
+                if constexpr (KS == 2) {
+                    if (nt > 1) {  // the groups' statistics; inv becomes 2^(m - M) / R, as with copies
+                        bars->stat[0][threadIdx.x] = m;
+                        bars->stat[1][threadIdx.x] = l;
+                        bars->stat[2][threadIdx.x] = lr;
+                        named_bar_sync(1, 256);
+                        const int x = threadIdx.x ^ 128;
+                        const float m2 = bars->stat[0][x], M = fmaxf(m, m2);
+                        const float f = (m == -INFINITY) ? 0.f : ex2(m - M);
+                        const float f2 = (m2 == -INFINITY) ? 0.f : ex2(m2 - M);
+                        l = f * l + f2 * bars->stat[1][x];
+                        none = l == 0.f;
+                        inv = f / (f * lr + f2 * bars->stat[2][x]);
+                        lse2 = none ? -INFINITY : M + lg2(l);
+                    }
+                }
 #pragma unroll 1
                 for (int c32 = 0; c32 < D / 32; ++c32) {
                     float v[32];
-                    if (nt > 0) {
+                    if (nt > 0 && has) {
                         uint32_t rr[32];
                         tmem_ld32(ob + c32 * 32, rr);
 #pragma unroll
@@ -986,10 +1013,27 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = 0.f;
                     }
+                    if constexpr (KS == 2) {  // the second group's O through shared memory
+                        if (nt > 1) {
+                            if (c32 > 0) named_bar_sync(1, 256);
+                            if (ks == 1)
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4)
+                                    *reinterpret_cast<float4 *>(other + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                            named_bar_sync(1, 256);
+                            if (ks == 0)
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4) {
+                                    const float4 y = *reinterpret_cast<const float4 *>(other + e);
+                                    v[e] += y.x, v[e + 1] += y.y, v[e + 2] += y.z, v[e + 3] += y.w;
+                                }
+                        }
+                    }
                     if (c32 == D / 32 - 1 && nt > 0) {
                         tc_fence_before();
                         mbar_arrive(&bars->o_empty);
                     }
+                    if (!writer) continue;
                     if (poison && live) {  // (a copy: v itself stays in registers)
                         float x[32];
 #pragma unroll
@@ -1001,7 +1045,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     if (it.whole) {
                         // through shared memory, so that a store covers 64 bytes of 8 rows
                         // instead of 16 bytes of 32 (16-byte chunks permuted by row pairs)
-                        uint4 *st = reinterpret_cast<uint4 *>(smem + C::OFF_MERGE + warp * 2048);
+                        uint4 *st = reinterpret_cast<uint4 *>(smem + C::OFF_MERGE + (KS == 1 ? warp : wq) * 2048);
                         __syncwarp();
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
@@ -1127,7 +1171,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     }
                 }
             }
-            if (mine && kw == 0) {
+            if (mine && kw == 0 && writer) {
                 if (it.whole)
                     p.lse[((long long)it.b * p.Hk * p.G + it.hk * p.G + head) * p.T + tok] =
                         lse2 * 0.69314718055994531f;

@@ -90,6 +90,8 @@ CASES = [
     (1, 1, 4, 1, 128, 64, [20000], BF, None, False),       # one long: cut into many pieces
     (1, 1, 1, 64, 64, 32, [9000], FP, None, True),
     (2, 2, 5, 20, 128, 32, [90, 256], FP, [20, 11], True), # one row tile, not repeated
+    (3, 2, 5, 20, 64, 32, [0, 256, 700], FP, [20, 1, 17], True),
+    (1, 1, 1, 100, 64, 64, [0], BF, None, False),
     (1, 1, 1, 129, 64, 16, [77], BF, None, True),          # masks of more than 128 columns
     (2, 1, 2, 200, 128, 32, [0, 500], FP, [200, 170], True),
     (1, 1, 130, 2, 64, 16, [140], BF, None, True),         # a token's heads in two row tiles
@@ -111,6 +113,8 @@ LONG = [
     (4, 8, 8, 13, 64, 64, [4000, 6100, 77, 2049], FP, None, False),
     (4, 8, 8, 20, 128, 16, [3500, 6000, 1, 4444], BF, [20, 17, 20, 4], True),
     (3, 8, 4, 70, 64, 128, [7000, 2500, 4100], BF, None, False),
+    (7, 8, 3, 33, 64, 16, [130, 6000, 0, 127, 2000, 90, 4000], BF, [33, 5, 1, 33, 20, 30, 33], True),
+    (90, 4, 5, 17, 64, 32, [(61 * i) % 400 for i in range(90)], FP, None, True),
     (8, 4, 4, 1, 128, 64, [16000] * 8, BF, None, False),   # tiles come in slower than they are used
     (8, 4, 4, 1, 64, 64, [20000] * 8, FP, None, False),
     (600, 4, 3, 1, 64, 16, [(97 * i) % 520 for i in range(600)], FP, None, False),
