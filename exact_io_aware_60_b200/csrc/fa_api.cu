@@ -863,11 +863,11 @@ bool make_query_map(CUtensorMap *m, const fa::Rows &r, int bf16, int d, int H, i
     return true;
 }
 
-template <int D, bool BF16, int REP, int RT>
+template <int D, bool BF16, int REP, int RT, int KS = 1>
 int launch_paged(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                  const fa::PagedParams &p, cudaStream_t st, int dev) {
-    using C = fa::PagedCfg<D, REP, RT>;
-    auto kern = fa::fa_paged_kernel<D, BF16, REP, RT>;
+    using C = fa::PagedCfg<D, REP, RT, KS>;
+    auto kern = fa::fa_paged_kernel<D, BF16, REP, RT, KS>;
     static std::atomic<int> smem_done[kMaxDevices];
     cudaError_t e = set_smem(kern, C::SMEM, smem_done, dev);
     if (e != cudaSuccess) {
@@ -1349,6 +1349,14 @@ int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *
     // 80 rows, 16 items of 4 tiles 12.9 and 12.6 (d = 128), of 5 tiles 11.6 and 12.8 (d = 64).
     const long long items = sh.row_tiles * Hk * B;
     p.uncut = cap_tiles <= (sh.rows > 64 ? 4 : items < 32 ? 6 : 10);
+    // Two groups of softmax warps (d = 64, one row tile of 65 to 128 rows) take less time a tile
+    // and more an item or piece of one: worth it from about 4 tiles a piece on, of which there
+    // are items + ctas.  One and two groups, 128 rows, us: 512 items of 2 tiles 26.1 and 27.3, of
+    // 5 tiles 48.5 and 48.8, of 8 tiles 62.6 and 58.3; 128 items of 5 tiles 18.9 and 19.5, of 10
+    // tiles 27.3 and 26.3, of 32 tiles 54.7 and 46.3; 8 items of 63 tiles 18.7 and 18.8, of 126
+    // tiles 23.9 and 22.7.  (The lengths are not known here: where a table has far more room
+    // than its sequences take, the choice costs up to 9%.)
+    const bool two_groups = d == 64 && sh.rows == 128 && items * cap_tiles >= 4 * (items + ctas);
     p.row_tiles = (int)sh.row_tiles;
     p.ctas = (int)std::min<double>(ctas, (double)sh.row_tiles * Hk * B * cap_tiles);
     p.scale_log2 = scale * 1.4426950408889634f;
@@ -1365,6 +1373,8 @@ int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *
                          : sh.rows == 64  ? launch_paged<D, BF, 2, 1>(FA_PAGED_ARGS) \
                          : sh.rows == 128 ? launch_paged<D, BF, 1, 1>(FA_PAGED_ARGS) \
                                           : launch_paged<D, BF, 1, 2>(FA_PAGED_ARGS))
+    if (two_groups)
+        return bf16 ? launch_paged<64, true, 1, 1, 2>(FA_PAGED_ARGS) : launch_paged<64, false, 1, 1, 2>(FA_PAGED_ARGS);
     if (d == 64) return bf16 ? FA_PAGED(64, true) : FA_PAGED(64, false);
     return bf16 ? FA_PAGED(128, true) : FA_PAGED(128, false);
 #undef FA_PAGED

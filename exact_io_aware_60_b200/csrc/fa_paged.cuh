@@ -33,10 +33,10 @@
 // REP lane quarters / halves, and each copy takes 1 / REP of the keys of every tile as a
 // softmax of its own (P is zero elsewhere); the copies are merged in the epilogue.  The
 // exponentials of a tile then take 1 / REP of the time.
-// At d = 64, where a tile's bytes take less than its 128 exponentials a row, one row tile has
-// two groups of softmax warps (KS = 2) that take the key tiles in turn, each with an O of its
-// own, merged in the epilogue (16 sequences of 4000 keys, 32 new tokens, 32 heads over 8: 55 us
-// with one group, 47 with two; a single tile costs 0.3 us more).
+// At d = 64, where a tile's bytes take less than its 128 exponentials a row, one row tile can
+// have two groups of softmax warps (KS = 2) that take the key tiles in turn, each with an O of
+// its own, merged in the epilogue (16 sequences of 4000 keys, 32 new tokens, 32 heads over 8:
+// 55 us with one group, 46 with two; of 600 keys 18.9 and 19.5, so that fa_fwd_paged chooses).
 // Many rows (RT = 2): two tiles of 128 rows share every K and V tile, each with softmax warps
 // of its own, so that one tile's products run beside the other's exponentials.
 #pragma once
@@ -68,12 +68,13 @@ struct PagedParams {
     float scale_log2;
 };
 
-template <int D, int REP, int RT>
+template <int D, int REP, int RT, int KS_ = 1>
 struct PagedCfg {
     static_assert(REP == 1 || RT == 1, "copies of one row tile, or two row tiles");
     static constexpr int BN = 128;              // keys per tile
     static constexpr int ROWS = 128 / REP;      // rows of a row tile
-    static constexpr int KS = (D == 64 && REP == 1 && RT == 1) ? 2 : 1;  // softmax groups of a row tile
+    static_assert(KS_ == 1 || (KS_ == 2 && D == 64 && REP == 1 && RT == 1), "two groups: one row tile at d = 64");
+    static constexpr int KS = KS_;              // softmax groups of a row tile
     static constexpr int HALVES = D / 64;
     static constexpr int QTILE = 128 * D * 2;
     static constexpr int TILE = BN * D * 2;     // K or V tile
@@ -84,12 +85,12 @@ struct PagedCfg {
     static constexpr int NV = (D == 64) ? (RT == 1 && KS == 1 ? 6 : 5) : (RT == 1 ? 3 : 2);
     // epilogue: REP > 1, a 32-column block of every row and copy, rows padded to 36 columns;
     // else 32 rows x 32 columns of 16 bits for each warp
-    static constexpr int MERGE = (REP > 1) ? 128 * 36 * 4 : RT * 4 * 2048 + (KS > 1 ? 128 * 36 * 4 : 0);
+    static constexpr int MERGE = (REP > 1) ? 128 * 36 * 4 : RT * 4 * 2048 + (KS > 1 ? 128 * 36 * 4 + 3 * 256 * 4 : 0);
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + RT * QTILE;
     static constexpr int OFF_MERGE = OFF_RING + (NK + NV) * TILE;
     static constexpr int OFF_BAR = OFF_MERGE + MERGE;
-    static constexpr int USED = OFF_BAR + 4864 + 8192;
+    static constexpr int USED = OFF_BAR + 3200 + 8192;
     static constexpr int SMEM = USED + 1024;
     static constexpr int SOFT = 4 * RT * KS;    // softmax warps
     // K and V come from a warp each where the registers allow one more: a box takes about
@@ -135,7 +136,7 @@ struct PagedBars {
     // Item t & 3 hides keys whose V is not finite.  (Four: the repairing warp reaches item
     // t + 4 only after the softmax of item t + 1 began.)
     int poison[4];
-    float stat[3][256];     // merge of copies or groups: m, l, l of the rounded weights
+    float stat[3][128];     // merge of copies: m, l, l of the rounded weights
     uint32_t mask[2][1024]; // per token of the piece, up to 128 bits: the new keys it sees
 };
 
@@ -455,11 +456,11 @@ __device__ __noinline__ uint32_t paged_bad_bits(uint32_t bad, int page_shift, in
     return bits;
 }
 
-template <int D, bool BF16, int REP, int RT>
-__global__ void __launch_bounds__(PagedCfg<D, REP, RT>::THREADS, 1)
+template <int D, bool BF16, int REP, int RT, int KS_>
+__global__ void __launch_bounds__(PagedCfg<D, REP, RT, KS_>::THREADS, 1)
 fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedParams p) {
-    using C = PagedCfg<D, REP, RT>;
+    using C = PagedCfg<D, REP, RT, KS_>;
     constexpr int ROWS = C::ROWS;
     constexpr int CW = C::STEP / REP; // keys of a step that one thread handles
     constexpr int SPT = C::SPT, KS = C::KS;
@@ -469,7 +470,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint8_t *sQ = smem + C::OFF_Q;
     uint8_t *ring = smem + C::OFF_RING;
     PagedBars *bars = reinterpret_cast<PagedBars *>(smem + C::OFF_BAR);
-    static_assert(sizeof(PagedBars) <= 4864 + 8192, "barrier area");
+    static_assert(sizeof(PagedBars) <= 3200 + 8192, "barrier area");
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
@@ -675,14 +676,15 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         // ------------------------------ pieces, Q loads, V repairs ----------------------
         PagedWalk<RT> walk;
         walk.init(p, blockIdx.x, lane);
-        bool ok = walk.step(p, bars, lane) && walk.step(p, bars, lane);
-        if (blockIdx.x == 0)
-            for (int b = lane; b < p.B; b += 32) page_lengths_check(p.pt, p.T, b);
+        bool ok = walk.step(p, bars, lane);
+        int loads = 0;
         int gj = 0, t = 0, served = 0, masks = 0;
         while (ok && paged_take(bars, np++, lane, true, it)) {
-            if (!(ok = walk.step(p, bars, lane))) break;
             const int nt = it.j1 - it.j0;
-            if (nt <= 0) continue;
+            if (nt <= 0) {
+                if (!(ok = walk.step(p, bars, lane))) break;
+                continue;
+            }
             if (t > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (t - 1) & 1))) break;
             if (lane == 0) {
                 // a box of TPT tokens x GP heads is a row tile (zeros behind the last token)
@@ -696,6 +698,11 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                                     it.tok0 + (RT > 1 ? i * p.TPT : 0), it.b);
             }
             __syncwarp();
+            ++loads;
+            // The next piece (after the first Q, which is waited for, the next two) is worked out
+            // behind the load: 512 items of 2 tiles, 128 rows, d = 64: 28.1 -> 26.1 us.
+            if (t == 0) ok = walk.step(p, bars, lane);
+            if (!(ok = ok && walk.step(p, bars, lane))) break;
             // The rows' masks as bits, one (token, 32 new keys) per lane at a time.
             if (p.tree != nullptr && p.T <= 128 && it.j1 * 128 > it.past) {
                 uint32_t *mask = bars->mask[masks & 1];
@@ -769,8 +776,10 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             ++t;
             gj += nt;
         }
+        if (blockIdx.x == 0)
+            for (int b = lane; b < p.B; b += 32) page_lengths_check(p.pt, p.T, b);
         // the last Q load has landed before the CTA's memory goes (at once unless a wait gave up)
-        if (t > 0) (void)mbar_wait(&bars->q_full, (t - 1) & 1);
+        if (loads > 0) (void)mbar_wait(&bars->q_full, (loads - 1) & 1);
     } else {
         // ------------------------------ softmax warps -----------------------------------
         constexpr int WPC = 4 / REP;                       // warps of one copy of the rows
@@ -807,7 +816,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             float l = 0.f;         // running sum
             float lr = 0.f;        // the same sum of the rounded weights
             const int i0 = KS == 1 ? 0 : ((n0 ^ ks) & 1);  // the group's first tile of the piece
-            const bool has = i0 < nt * SPT;
+            const bool has = KS == 1 ? nt > 0 : i0 < nt;
             for (int i = i0; ok && i < nt * SPT; i += KS) {
                 const int n = n0 + i, b = sb_of(n, ti);
                 const int kt = i % SPT * C::STEP + kw * CW;        // this thread's keys of the tile
@@ -987,24 +996,25 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 float *other = reinterpret_cast<float *>(smem + C::OFF_MERGE + 4 * 2048) + row * 36;
                 if constexpr (KS == 2) {
                     if (nt > 1) {  // the groups' statistics; inv becomes 2^(m - M) / R, as with copies
-                        bars->stat[0][threadIdx.x] = m;
-                        bars->stat[1][threadIdx.x] = l;
-                        bars->stat[2][threadIdx.x] = lr;
+                        float *stat = reinterpret_cast<float *>(smem + C::OFF_MERGE + 4 * 2048 + 128 * 36 * 4);
+                        stat[threadIdx.x] = m;
+                        stat[256 + threadIdx.x] = l;
+                        stat[512 + threadIdx.x] = lr;
                         named_bar_sync(1, 256);
                         const int x = threadIdx.x ^ 128;
-                        const float m2 = bars->stat[0][x], M = fmaxf(m, m2);
+                        const float m2 = stat[x], M = fmaxf(m, m2);
                         const float f = (m == -INFINITY) ? 0.f : ex2(m - M);
                         const float f2 = (m2 == -INFINITY) ? 0.f : ex2(m2 - M);
-                        l = f * l + f2 * bars->stat[1][x];
+                        l = f * l + f2 * stat[256 + x];
                         none = l == 0.f;
-                        inv = f / (f * lr + f2 * bars->stat[2][x]);
+                        inv = f / (f * lr + f2 * stat[512 + x]);
                         lse2 = none ? -INFINITY : M + lg2(l);
                     }
                 }
 #pragma unroll 1
                 for (int c32 = 0; c32 < D / 32; ++c32) {
                     float v[32];
-                    if (nt > 0 && has) {
+                    if (has) {
                         uint32_t rr[32];
                         tmem_ld32(ob + c32 * 32, rr);
 #pragma unroll
@@ -1033,7 +1043,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         tc_fence_before();
                         mbar_arrive(&bars->o_empty);
                     }
-                    if (!writer) continue;
+                    if (KS == 2 && !writer) continue;
                     if (poison && live) {  // (a copy: v itself stays in registers)
                         float x[32];
 #pragma unroll

@@ -136,6 +136,64 @@ def test_long_shares(case):
     assert torch.isfinite(o.float()).all()
 
 
+def widen(c, tiles):
+    """The same problem in a table with room for `tiles` tiles of 128 keys; the entries behind the
+    sequences' are no pages at all.  (The room decides between one and two softmax groups, and
+    whether items are cut.)"""
+    B, blocks = c["table"].shape
+    room = -(-tiles * 128 // c["kc"].shape[2])
+    assert room >= blocks
+    c["table"] = torch.cat([c["table"], torch.full((B, room - blocks), -1, dtype=torch.int32)], 1)
+    return c
+
+
+@pytest.mark.parametrize("case", [
+    (3, 2, 5, 20, 64, 32, [0, 256, 700], FP, [20, 1, 17], True),
+    (1, 1, 1, 100, 64, 64, [0], BF, None, False),          # one tile, the second group has none
+    (2, 1, 3, 40, 64, 16, [100, 128], BF, None, False),    # two tiles, the last short
+    (2, 2, 4, 32, 64, 8, [125, 383], FP, [0, 32], True),
+    (1, 2, 128, 1, 64, 32, [1500], BF, None, False),
+    (1, 1, 13, 9, 64, 128, [5000], FP, None, True),
+], ids=lambda c: "-".join(str(x) for x in c[:6]))
+def test_more_room_than_keys(case):
+    B, Hk, G, T, d, page, lens, dtype, new, tree = case
+    c = problem(B, Hk, G, T, d, page, lens, dtype, new=new, tree=tree, seed=len(lens) + T)
+    tight, tight_lse = against_reference(c)
+    o, lse = against_reference(widen(c, 800))
+    assert torch.equal(torch.isneginf(lse), torch.isneginf(tight_lse))
+    empty = torch.isneginf(lse)
+    assert torch.all(o[empty] == 0) and torch.all(tight[empty] == 0)
+
+
+def test_many_short_in_a_wide_table():
+    B = 90
+    c = problem(B, 4, 5, 17, 64, 32, [(61 * i) % 400 for i in range(B)], FP, tree=True, seed=B)
+    against_reference(widen(c, 12))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_hidden_keys_in_a_wide_table(value):
+    c = widen(problem(1, 1, 5, 20, 64, 16, [250], FP, tree=True, seed=6), 800)
+    s = 250 + 5
+    page, row = int(c["table"][0, s // 16]), s % 16
+    clean, _ = against_reference(c)
+    c["vc"][page, 0, row, 7] = value
+    c["kc"][page, 0, row] = float("nan")
+    sees = c["tree"][0, :, 5] != 0
+    o, lse = run(c)
+    assert sees.any() and (~sees).any()
+    assert torch.equal(o[0, :, ~sees], clean[0, :, ~sees])
+    assert torch.isnan(o[0, :, sees]).all() and torch.isnan(lse[0, :, sees]).all()
+
+
+def test_rows_that_see_nothing_in_a_wide_table():
+    c = widen(problem(3, 1, 3, 40, 64, 16, [0, 5, 200], FP, tree=True, seed=4), 400)
+    c["tree"][0] = 0
+    c["tree"][1, 20] = 0
+    o, lse = against_reference(c)
+    assert torch.all(o[0] == 0) and torch.all(torch.isneginf(lse[0]))
+
+
 @pytest.mark.parametrize("T", [1, 3, 40])
 def test_rows_that_see_nothing(T):
     c = problem(3, 1, 3, T, 64, 16, [0, 5, 200], FP, tree=True, seed=4)
