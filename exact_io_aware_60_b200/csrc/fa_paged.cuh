@@ -84,15 +84,18 @@ struct PagedCfg {
     static constexpr int NK = (D == 64) ? 5 : 2;
     static constexpr int NV = (D == 64) ? (RT == 1 && KS == 1 ? 6 : 5) : (RT == 1 ? 3 : 2);
     // epilogue: REP > 1, a 32-column block of every row and copy, rows padded to 36 columns;
-    // else 32 rows x 32 columns of 16 bits for each warp
-    static constexpr int MERGE = (REP > 1) ? 128 * 36 * 4 : RT * 4 * 2048 + (KS > 1 ? 128 * 36 * 4 + 3 * 256 * 4 : 0);
+    // else 32 rows x 32 columns of 16 bits for each softmax warp (with two groups too: the one
+    // that writes changes from piece to piece, and no barrier stands between a piece of one tile,
+    // which its group writes, and a piece of none, which the first does)
+    static constexpr int SOFT = 4 * RT * KS;    // softmax warps
+    static constexpr int STAGE = SOFT * 2048;
+    static constexpr int MERGE = (REP > 1) ? 128 * 36 * 4 : STAGE + (KS > 1 ? 128 * 36 * 4 + 3 * 256 * 4 : 0);
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + RT * QTILE;
     static constexpr int OFF_MERGE = OFF_RING + (NK + NV) * TILE;
     static constexpr int OFF_BAR = OFF_MERGE + MERGE;
     static constexpr int USED = OFF_BAR + 3200 + 8192;
     static constexpr int SMEM = USED + 1024;
-    static constexpr int SOFT = 4 * RT * KS;    // softmax warps
     // K and V come from a warp each where the registers allow one more: a box takes about
     // 45 ns to issue, and pages of 16 tokens are 32 boxes a tile at d = 128.
     static constexpr int LOADERS = (SOFT == 4) ? 2 : 1;
@@ -993,10 +996,10 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             };
             const long long prow0 = (long long)it.slot * (RT * ROWS) + ti * ROWS;  // first row of the partial
             if constexpr (REP == 1) {
-                float *other = reinterpret_cast<float *>(smem + C::OFF_MERGE + 4 * 2048) + row * 36;
+                float *other = reinterpret_cast<float *>(smem + C::OFF_MERGE + C::STAGE) + row * 36;
                 if constexpr (KS == 2) {
                     if (nt > 1) {  // the groups' statistics; inv becomes 2^(m - M) / R, as with copies
-                        float *stat = reinterpret_cast<float *>(smem + C::OFF_MERGE + 4 * 2048 + 128 * 36 * 4);
+                        float *stat = reinterpret_cast<float *>(smem + C::OFF_MERGE + C::STAGE + 128 * 36 * 4);
                         stat[threadIdx.x] = m;
                         stat[256 + threadIdx.x] = l;
                         stat[512 + threadIdx.x] = lr;
@@ -1055,7 +1058,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     if (it.whole) {
                         // through shared memory, so that a store covers 64 bytes of 8 rows
                         // instead of 16 bytes of 32 (16-byte chunks permuted by row pairs)
-                        uint4 *st = reinterpret_cast<uint4 *>(smem + C::OFF_MERGE + (KS == 1 ? warp : wq) * 2048);
+                        uint4 *st = reinterpret_cast<uint4 *>(smem + C::OFF_MERGE + warp * 2048);
                         __syncwarp();
 #pragma unroll
                         for (int e = 0; e < 4; ++e)

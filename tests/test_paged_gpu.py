@@ -171,6 +171,26 @@ def test_many_short_in_a_wide_table():
     against_reference(widen(c, 12))
 
 
+@pytest.mark.parametrize("B,Hk,lens,every", [
+    (256, 2, [60], 2),
+    (256, 8, [60], 2),
+    (200, 4, [(37 * i) % 108 for i in range(200)], 3),
+], ids=lambda c: str(len(c)) if isinstance(c, list) else str(c))
+def test_short_sequences_next_to_finished_ones(B, Hk, lens, every):
+    """Two softmax groups: pieces of one tile, written by the group that worked on them, and
+    pieces of sequences without a new token, of no tile, behind one another in one CTA."""
+    T, G = 20, 5
+    new = [T if i % every == 0 else 0 for i in range(B)]
+    c = widen(problem(B, Hk, G, T, 64, 16, [lens[i % len(lens)] for i in range(B)], BF, new=new, seed=B + Hk), 8)
+    o, lse = against_reference(c)
+    x = on_gpu(c)
+    ws = fa.paged_workspace_for(x["q"], Hk)
+    for _ in range(50):
+        again, lse_again = fa.forward_paged(x["q"], x["kc"], x["vc"], x["table"], x["cache_len"],
+                                            new_len=x["new_len"], workspace=ws)
+        assert torch.equal(again, o) and torch.equal(lse_again, lse)
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 def test_hidden_keys_in_a_wide_table(value):
     c = widen(problem(1, 1, 5, 20, 64, 16, [250], FP, tree=True, seed=6), 800)
