@@ -1204,6 +1204,9 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 
 // Merges the pieces of the items that were cut: with the pieces' log-sum-exps L_s (base 2),
 //   LSE = M + log2 sum_s 2^(L_s - M), O = sum_s 2^(L_s - LSE) O_s.
+// An O_s may be infinite (a visible key's value is), and 0 * inf would be NaN: rounds are filled
+// up with zeros, and 2^x, which is 0 from x = -127 on, gets the smallest fp32 number added: less
+// than 5e-7 of the largest 16-bit value, nothing beside a weight that counts.
 // A share leaves at most one item unfinished that it began: grid.x = shares.  The item, its
 // pieces and their places are worked out before the wait for the attention kernel (which
 // triggers this launch behind its own wait, so that the lengths are final by then).
@@ -1246,6 +1249,7 @@ __global__ void __launch_bounds__(256, 4) fa_paged_merge_kernel(const __grid_con
     constexpr int E = TRANS ? D / 8 : D / 32;             // columns of a thread
     constexpr int R = TRANS ? 1 : (REP == 4 ? 1 : 2), U = TRANS ? 4 : (REP == 4 ? 8 : 3);
     constexpr int NR = TRANS ? 1 : (REP == 4 ? 4 : 8);    // rows of a thread
+    constexpr float kTiny = 1.401298464324817e-45f;       // 2^-149
 #pragma unroll 1
     for (int k = 0; k < NR; k += R) {
         int row[R], tok[R], head[R];
@@ -1303,17 +1307,17 @@ __global__ void __launch_bounds__(256, 4) fa_paged_merge_kernel(const __grid_con
                 float M1 = M[j];
 #pragma unroll
                 for (int u = 0; u < U; ++u) M1 = fmaxf(M1, ls[u][j]);
-                const float alpha = M[j] == -INFINITY ? 0.f : ex2(M[j] - M1);
+                const float alpha = M[j] == -INFINITY ? 0.f : ex2(M[j] - M1) + kTiny;
                 M[j] = M1;
                 sum[j] *= alpha;
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[j][e] *= alpha;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const float w = ls[u][j] == -INFINITY ? 0.f : ex2(ls[u][j] - M1);  // (NaN is carried on)
+                    const float w = ls[u][j] == -INFINITY ? 0.f : ex2(ls[u][j] - M1) + kTiny;  // (NaN is carried on)
                     sum[j] += w;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[j][e] = fmaf(w, v[u][j][e], acc[j][e]);
+                    for (int e = 0; e < E; ++e) acc[j][e] = fmaf(w, s0 + u <= c1 ? v[u][j][e] : 0.f, acc[j][e]);
                 }
             }
         }

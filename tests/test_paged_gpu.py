@@ -263,6 +263,60 @@ def test_not_finite_values_in_hidden_keys(value, T, G):
         assert torch.isnan(bad).all()
 
 
+FORMS = [(5, 4, 64), (5, 4, 128), (12, 5, 64), (12, 5, 128), (20, 5, 64), (20, 5, 128), (50, 4, 64), (50, 4, 128)]
+
+
+def spiked(c, slot):
+    """One key that every row puts all its weight on (some 400 nats above the others)."""
+    page = c["kc"].shape[2]
+    c["q"][..., 0] = 4.0
+    c["kc"][int(c["table"][0, slot // page]), :, slot % page, 0] = 100.0 * c["q"].shape[-1] ** 0.5
+    return c
+
+
+def against_infinite(c, marks):
+    """Sequence 0 of the problem with values that are not finite: marks = [(slot, column, value)],
+    all key/value heads.  A row that sees such a key has their sum in the column, however small the
+    key's weight (in 64 bits all are above 0); everything else is as with finite values there."""
+    page, past = c["kc"].shape[2], int(c["cache_len"][0])
+    wo, wl, ob, lb = R.paged(c["q"], c["kc"], c["vc"], c["table"], c["cache_len"], c["new_len"],
+                             c["tree"], c["q"].shape[-1] ** -0.5)
+    ob = ob + R.rounding(wo, c["q"].dtype)
+    c = dict(c, vc=c["vc"].clone())
+    n = c["q"].shape[2] if c["new_len"] is None else int(c["new_len"][0])
+    hit = np.zeros(wo.shape)
+    for slot, col, value in marks:
+        c["vc"][int(c["table"][0, slot // page]), :, slot % page, col] = value
+        x = slot - past
+        with np.errstate(all="ignore"):
+            for t in range(n):
+                if x < 0 or (x <= t if c["tree"] is None else bool(c["tree"][0, t, x])):
+                    hit[0, :, t, col] += value
+    assert (hit != 0).any()
+    o, lse = run(c)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK
+    R.check("o", o, np.where(hit != 0, hit, wo), ob)
+    R.check("lse", lse, wl, lb)
+    return o, hit
+
+
+@pytest.mark.parametrize("spike", [None, 10], ids=["even", "spiked"])
+@pytest.mark.parametrize("T,G,d", FORMS)
+@pytest.mark.parametrize("wide", [False, True], ids=["tight", "wide"])
+def test_infinite_values_of_new_keys_in_cut_items(T, G, d, wide, spike):
+    """An infinite V in a drafted token of an item in many pieces: that infinity in the rows that
+    see it, however small its weight, nothing in the others."""
+    past = 5000
+    c = problem(1, 1, G, T, d, 16, [past], BF if T == 12 else FP, tree=True, seed=T + d)
+    if wide:
+        c = widen(c, 800)
+    if spike is not None:
+        c = spiked(c, spike)
+    _, hit = against_infinite(c, [(past + T // 2, 7, float("inf")), (past + T // 2, d - 1, float("-inf"))])
+    assert (hit[0, 0, :, 7] == 0).any()
+
+
 def test_not_finite_values_in_a_chain():
     c = problem(1, 2, 2, 140, 128, 32, [60], BF, seed=7)
     clean = {n: None if t is None else t.clone() for n, t in c.items()}
