@@ -1204,9 +1204,9 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 
 // Merges the pieces of the items that were cut: with the pieces' log-sum-exps L_s (base 2),
 //   LSE = M + log2 sum_s 2^(L_s - M), O = sum_s 2^(L_s - LSE) O_s.
-// An O_s may be infinite (a visible key's value is), and 0 * inf would be NaN: rounds are filled
-// up with zeros, and 2^x, which is 0 from x = -127 on, gets the smallest fp32 number added: less
-// than 5e-7 of the largest 16-bit value, nothing beside a weight that counts.
+// An O_s may be infinite (a visible key's value is), and 0 * inf would be NaN, so no weight is 0:
+// 2^x, which is from x = -127 on and for the repeats of the last piece that fill up a round, gets
+// the smallest fp32 number added (2^-149 of the largest 16-bit value is below 5e-7).
 // A share leaves at most one item unfinished that it began: grid.x = shares.  The item, its
 // pieces and their places are worked out before the wait for the attention kernel (which
 // triggers this launch behind its own wait, so that the lengths are final by then).
@@ -1245,9 +1245,11 @@ __global__ void __launch_bounds__(256, 4) fa_paged_merge_kernel(const __grid_con
     if (!cut) return;
     // Each round takes U pieces of R rows, log-sum-exps and outputs together, into a running
     // maximum and sum: one wait on L2 (about 0.7 us) a round.  Few rows come in many pieces
-    // (decoding), many rows in few.
+    // (decoding), many rows in few.  (Three pieces at d = 128: four do not fit 64 registers.  128
+    // rows, 16 sequences of 4000 keys: 61.7 us with three, 63.0 with four, 60.7 with two; one item
+    // in 148 pieces: 48.1 with three, 50.2 with four, 57.1 with two.)
     constexpr int E = TRANS ? D / 8 : D / 32;             // columns of a thread
-    constexpr int R = TRANS ? 1 : (REP == 4 ? 1 : 2), U = TRANS ? 4 : (REP == 4 ? 8 : 3);
+    constexpr int R = TRANS ? 1 : (REP == 4 ? 1 : 2), U = TRANS ? (D == 128 ? 3 : 4) : (REP == 4 ? 8 : 3);
     constexpr int NR = TRANS ? 1 : (REP == 4 ? 4 : 8);    // rows of a thread
     constexpr float kTiny = 1.401298464324817e-45f;       // 2^-149
 #pragma unroll 1
@@ -1270,7 +1272,7 @@ __global__ void __launch_bounds__(256, 4) fa_paged_merge_kernel(const __grid_con
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             sum[j] = 0.f;
-            M[j] = -INFINITY;
+            M[j] = -3.402823466e38f;  // (finite, so that the differences below are numbers)
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[j][e] = 0.f;
         }
@@ -1307,31 +1309,32 @@ __global__ void __launch_bounds__(256, 4) fa_paged_merge_kernel(const __grid_con
                 float M1 = M[j];
 #pragma unroll
                 for (int u = 0; u < U; ++u) M1 = fmaxf(M1, ls[u][j]);
-                const float alpha = M[j] == -INFINITY ? 0.f : ex2(M[j] - M1) + kTiny;
+                const float alpha = ex2(M[j] - M1) + kTiny;
                 M[j] = M1;
                 sum[j] *= alpha;
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[j][e] *= alpha;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const float w = ls[u][j] == -INFINITY ? 0.f : ex2(ls[u][j] - M1) + kTiny;  // (NaN is carried on)
+                    const float w = ex2(ls[u][j] - M1) + kTiny;  // (NaN is carried on)
                     sum[j] += w;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[j][e] = fmaf(w, s0 + u <= c1 ? v[u][j][e] : 0.f, acc[j][e]);
+                    for (int e = 0; e < E; ++e) acc[j][e] = fmaf(w, v[u][j][e], acc[j][e]);
                 }
             }
         }
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             if (!in[j]) continue;
-            const float inv = sum[j] == 0.f ? 0.f : 1.f / sum[j];
+            const bool none = sum[j] < 0.5f;  // no piece with a key: else the largest weight is 1
+            const float inv = none ? 0.f : 1.f / sum[j];
             const int h = hk * p.G + head[j];
             uint32_t *o = reinterpret_cast<uint32_t *>(const_cast<uint16_t *>(p.o.p) + b * p.o.sb + h * p.o.sh +
                                                        tok[j] * p.o.st + (TRANS ? warp : lane) * E);
             uint32_t w[E / 2];
 #pragma unroll
             for (int e = 0; e < E / 2; ++e)
-                w[e] = sum[j] == 0.f ? 0u : pack2<BF16>(acc[j][2 * e] * inv, acc[j][2 * e + 1] * inv);
+                w[e] = none ? 0u : pack2<BF16>(acc[j][2 * e] * inv, acc[j][2 * e + 1] * inv);
             if constexpr (E / 2 >= 4) {
 #pragma unroll
                 for (int e = 0; e < E / 8; ++e)
@@ -1343,7 +1346,7 @@ __global__ void __launch_bounds__(256, 4) fa_paged_merge_kernel(const __grid_con
             }
             if (TRANS ? warp == 0 : lane == 0)
                 p.lse[((long long)b * p.Hk * p.G + h) * p.T + tok[j]] =
-                    sum[j] == 0.f ? -INFINITY : (M[j] + lg2(sum[j])) * 0.69314718055994531f;
+                    none ? -INFINITY : (M[j] + lg2(sum[j])) * 0.69314718055994531f;
         }
     }
 }
