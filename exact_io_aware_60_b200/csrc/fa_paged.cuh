@@ -421,24 +421,110 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
-// Adds the values that are not finite, columns col .. col + n - 1, of the new keys that token
-// tk sees among the piece's to v.  (Out of line, as is the next: rare, and the code that every
-// piece runs through comes in from memory at each launch.)
-template <bool BF16>
-__device__ __noinline__ void paged_add_not_finite(const PagedParams &p, const PagedSeg &it, float *v, int n,
-                                                  int col, int tk) {
-    for (int j = max(it.past, it.j0 * 128); j < min(it.total, it.j1 * 128); ++j) {
-        const int x = j - it.past;
-        const bool seen = p.tree ? p.tree[it.b * p.tree_sb + (long long)tk * p.T + x] != 0 : x <= tk;
-        const int id = p.pt.table[(long long)it.b * p.pt.max_blocks + (j >> p.pt.page_shift)];
-        if (!seen || id < 0 || id >= p.pt.num_pages) continue;
-        const uint16_t *src = p.vc.p + id * p.vc.sb + it.hk * p.vc.sh +
-                              (j & ((1 << p.pt.page_shift) - 1)) * p.vc.st + col;
-        for (int e = 0; e < n; ++e) {
-            const uint32_t w = src[e];
-            if (not_finite2<BF16>(w) & 0xffffu) v[e] += unpack2<BF16>(w).x;
+// The row of key j in the value cache (nullptr: its page lies outside).
+__device__ __forceinline__ const uint16_t *paged_value(const PagedParams &p, const PagedSeg &it, int j) {
+    const int id = p.pt.table[(long long)it.b * p.pt.max_blocks + (j >> p.pt.page_shift)];
+    if (id < 0 || id >= p.pt.num_pages) return nullptr;
+    return p.vc.p + id * p.vc.sb + it.hk * p.vc.sh + (j & ((1 << p.pt.page_shift) - 1)) * p.vc.st;
+}
+
+// Puts the values that are not finite of the keys that a row sees into its output or piece: their
+// sum, as every visible key's weight is above 0, where P V has 0 * inf = NaN for weights that
+// round to 0 and for the keys of other copies, and nothing for values that the repair cleared.
+// A whole warp calls this for what its threads stored: rows r0, r0 + step, .. < used of row tile
+// ti and n columns from c4 on (in every block of 32, or `once`: in c4's).  held: some output of
+// the warp is not finite, so the keys that all rows see are gone over (32 at a time, one per
+// lane); cleared: so are the others.  ok: a row's weights are numbers (copies: its sums, `sums`).
+// (Out of line, as are the next: rare, and the code that every piece runs through comes in from
+// memory at each launch.)
+template <int D, bool BF16, int REP, int RT>
+__device__ __noinline__ void paged_put_not_finite(const PagedParams &p, const PagedSeg &it, int ti, int r0, int step,
+                                                  int used, int c4, int n, bool once, bool held, bool cleared,
+                                                  bool ok, const float *sums) {
+    constexpr int ROWS = 128 / REP;
+    const int k0 = it.j0 * 128, k1 = min(it.total, it.j1 * 128);
+    const int mid = max(k0, min(k1, it.open(p, it.tok0)));
+#pragma unroll 1
+    for (int cb = 0; cb < D; cb += 32) {
+        float y[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = 0.f;
+        if (held) {
+#pragma unroll 1
+            for (int j = k0 + (int)(threadIdx.x & 31); j < mid; j += 32) {
+                const uint16_t *src = paged_value(p, it, j);
+                if (src == nullptr) continue;
+                uint4 x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = reinterpret_cast<const uint4 *>(src + cb)[e];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = unpack2<BF16>(w[i]);
+                        const uint32_t bad = not_finite2<BF16>(w[i]);
+                        if (bad & 0xffffu) y[8 * e + 2 * i] += f.x;
+                        if (bad >> 16) y[8 * e + 2 * i + 1] += f.y;
+                    }
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                for (int o = 16; o > 0; o >>= 1) y[e] += __shfl_xor_sync(0xffffffffu, y[e], o);
+        }
+        if (once && c4 >> 5 != cb >> 5) continue;
+#pragma unroll 1
+        for (int r = r0; r < used; r += step) {
+            const int tl = r * p.gp_magic >> 16, tok = it.tok0 + ti * p.TPT + tl, h = it.g0 + (r - tl * p.GP);
+            if (tl >= p.TPT || tok >= it.fresh || h >= p.G) continue;
+            if (REP > 1) {
+                float l = 0.f;
+                for (int k = 0; k < REP; ++k) l += sums[k * ROWS + r];
+                ok = l > 0.f;
+            }
+            if (!ok) continue;
+            float s[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = y[e];
+            const int e0 = c4 & 31;
+#pragma unroll 1
+            for (int j = mid; cleared && j < k1; ++j) {
+                const int x = j - it.past;
+                if (!(p.tree ? p.tree[it.b * p.tree_sb + (long long)tok * p.T + x] != 0 : x <= tok)) continue;
+                const uint16_t *src = paged_value(p, it, j);
+                if (src == nullptr) continue;
+#pragma unroll 4
+                for (int e = e0; e < e0 + n; ++e) {
+                    const uint32_t w = src[cb + e];
+                    if (not_finite2<BF16>(w) & 0xffffu) s[e] += unpack2<BF16>(w).x;
+                }
+            }
+            const long long at = (long long)it.slot * (RT * ROWS) + ti * ROWS;
+#pragma unroll 1
+            for (int e = e0; e < e0 + n; ++e) {
+                const int c = cb + e;
+                if (s[e] == 0.f) continue;
+                if (it.whole)
+                    const_cast<uint16_t *>(p.o.p)[it.b * p.o.sb + (it.hk * p.G + h) * p.o.sh + tok * p.o.st + c] =
+                        (uint16_t)pack2<BF16>(s[e], s[e]);
+                else if (REP > 1)
+                    p.part_o[(at + r) * D + c] = s[e];
+                else
+                    p.part_o[at * D + ((c >> 2) * ROWS + r) * 4 + (c & 3)] = s[e];
+            }
         }
     }
+}
+
+// NaN if one of N values is not finite, else 0.
+template <int N>
+__device__ __forceinline__ float paged_finite(const float (&v)[N]) {
+    float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < N; ++e) z[e & 3] = fmaf(v[e], 0.f, z[e & 3]);
+    return (z[0] + z[1]) + (z[2] + z[3]);
 }
 
 // New keys x0 .. x0 + 31 (x0 > -32) that token tok sees, from a mask of more than 128 columns.
@@ -988,8 +1074,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             float inv = none ? 0.f : 1.f / lr;
             const bool writer = KS == 1 || (nt == 1 ? has : ks == 0);  // (one tile: its group alone)
             float lse2 = none ? -INFINITY : m + lg2(l);
-            // Values that the repair cleared reach the rows that do see them (rare: only where
-            // a new key's V is not finite, and slow).
+            // Values that the repair cleared reach the rows that do see them (see paged_put_not_finite).
             const bool poison = nt > 0 && it.repair(p, it.j1 - 1) && bars->poison[t & 3] != 0;
             auto out_row = [&](int h, int tk) {
                 return const_cast<uint16_t *>(p.o.p) + it.b * p.o.sb + (it.hk * p.G + h) * p.o.sh + tk * p.o.st;
@@ -1014,6 +1099,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         lse2 = none ? -INFINITY : M + lg2(l);
                     }
                 }
+                float z = 0.f;  // NaN where an output is not finite
 #pragma unroll 1
                 for (int c32 = 0; c32 < D / 32; ++c32) {
                     float v[32];
@@ -1047,14 +1133,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         mbar_arrive(&bars->o_empty);
                     }
                     if (KS == 2 && !writer) continue;
-                    if (poison && live) {  // (a copy: v itself stays in registers)
-                        float x[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = v[e];
-                        paged_add_not_finite<BF16>(p, it, x, 32, c32 * 32, tok);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = x[e];
-                    }
+                    z += paged_finite(v);
                     if (it.whole) {
                         // through shared memory, so that a store covers 64 bytes of 8 rows
                         // instead of 16 bytes of 32 (16-byte chunks permuted by row pairs)
@@ -1085,6 +1164,13 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                             dst[e * ROWS] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     }
                 }
+                const bool held = __any_sync(0xffffffffu, live && z != 0.f);
+                if (writer && (poison || held)) {
+                    const PagedSeg piece = it;  // (copies: the piece stays in registers)
+                    __syncwarp();
+                    paged_put_not_finite<D, BF16, REP, RT>(p, piece, ti, row, 128, 128, 0, 32, false, held, poison,
+                                                           l > 0.f, nullptr);
+                }
             } else {
                 // The copies meet in shared memory (the vote above is also the barrier behind
                 // the last piece's reads): first their maxima and sums, then O scaled by
@@ -1110,7 +1196,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         dst[e] = it.whole ? (void *)(out_row(h, dtok[e]) + c4)
                                           : (void *)(p.part_o + (prow0 + r) * D + c4);
                 }
-                float scale = 0.f;
+                float scale = 0.f, z = 0.f;  // z: NaN where an output is not finite
                 if (nt > 0) {
                     bars->stat[0][x] = m;
                     bars->stat[1][x] = l;
@@ -1170,11 +1256,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                                 v[3] += y.w;
                             }
                         }
-                        if (poison && dtok[e] < it.fresh) {
-                            float y[4] = {v[0], v[1], v[2], v[3]};
-                            paged_add_not_finite<BF16>(p, it, y, 4, c0 + c4, dtok[e]);
-                            v[0] = y[0], v[1] = y[1], v[2] = y[2], v[3] = y[3];
-                        }
+                        z += paged_finite(v);
                         if (it.whole)
                             *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst[e]) + c0) =
                                 make_uint2(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]));
@@ -1182,6 +1264,12 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                             *reinterpret_cast<float4 *>(static_cast<float *>(dst[e]) + c0) =
                                 make_float4(v[0], v[1], v[2], v[3]);
                     }
+                }
+                const bool held = __any_sync(0xffffffffu, z != 0.f);
+                if (poison || held) {
+                    const PagedSeg piece = it;  // (copies: the piece stays in registers)
+                    paged_put_not_finite<D, BF16, REP, RT>(p, piece, 0, x >> qs, 128 >> qs, used, c4, 4, once, held,
+                                                           poison, false, bars->stat[1]);
                 }
             }
             if (mine && kw == 0 && writer) {

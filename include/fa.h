@@ -402,7 +402,9 @@ FA_API int fa_kv_append(const void *k, const void *v, void *k_cache, void *v_cac
  *                 device: call both on the same one.
  * Rows that see no key, rows t >= new_len[b] among them, get O = 0, LSE = -inf.  Slots from
  * cache_len[b] + new_len[b] on are never used, whatever they hold; keys that a row's mask
- * hides do not touch that row either, infinities and NaN in them included.  Lengths are
+ * hides do not touch that row either, infinities and NaN in them included.  An infinite value
+ * of a key that a row sees is that row's output in its column however small the weight (NaN
+ * where both signs meet, or where a value or a score is NaN).  Lengths are
  * clamped to 0 <= cache_len <= max_blocks * page_size, 0 <= new_len <= T and a sum within the
  * table; page numbers outside [0, num_pages) make their keys invisible; both report
  * FA_ERR_BAD_PAGE in the device status word.

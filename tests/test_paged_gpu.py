@@ -317,6 +317,47 @@ def test_infinite_values_of_new_keys_in_cut_items(T, G, d, wide, spike):
     assert (hit[0, 0, :, 7] == 0).any()
 
 
+@pytest.mark.parametrize("past", [90, 5000])
+@pytest.mark.parametrize("spike", [None, "low", "high"])
+@pytest.mark.parametrize("T,G,d", [(1, 1, 64), (1, 8, 128), *FORMS])
+@pytest.mark.parametrize("wide", [False, True], ids=["tight", "wide"])
+def test_infinite_values_of_held_keys(T, G, d, wide, spike, past):
+    """Infinite values of keys that every row sees, in an uncut and a cut item: held ones in
+    different places of a tile, and a single new token's own.  low, high: the weight of all other
+    keys rounds to 0, first or last key."""
+    dtype = BF if (T + d) % 3 == 0 else FP
+    c = problem(1, 2, G, T, d, 16, [past], dtype, seed=T + d + past)
+    if wide:
+        c = widen(c, 800)
+    if spike is not None:
+        c = spiked(c, 3 if spike == "low" else past - 1)
+    inf = float("inf")
+    marks = [(past // 2, 0, inf), (past // 2 + 33, 9, -inf), (past - 2, 31, inf), (1, 32, -inf),
+             (past // 2, 40, inf), (past // 2 + 1, 40, inf), (past - 2, 41, inf), (2, 41, -inf),
+             (past, d - 1, inf), (past // 3, d - 2, float("nan"))]
+    against_infinite(c, marks)
+
+
+def test_weights_that_are_not_finite_stay_so():
+    """A visible key whose score is NaN makes its rows NaN, infinite values or not; a row that sees
+    nothing stays empty."""
+    for T, G, d in FORMS:
+        c = problem(1, 1, G, T, d, 16, [200], BF, tree=True, seed=T)
+        c["tree"][0] = torch.tril(torch.ones((T, T), dtype=torch.uint8))
+        page, row = int(c["table"][0, 201 // 16]), 201 % 16
+        c["kc"][page, 0, row] = float("nan")
+        c["vc"][int(c["table"][0, 3]), 0, 0, 5] = float("inf")
+        o, lse = run(c)
+        assert torch.isnan(o[0, :, 1:]).all() and torch.isnan(lse[0, :, 1:]).all()
+        assert torch.all(o[0, :, 0, 5] == float("inf")) and torch.isfinite(lse[0, :, 0]).all()
+        c = problem(1, 1, G, T, d, 16, [0], BF, tree=True, seed=T)
+        c["tree"][0, 0] = 0
+        c["vc"][int(c["table"][0, 0]), 0, 1, 5] = float("inf")
+        o, lse = run(c)
+        assert torch.all(o[0, :, 0] == 0) and torch.all(torch.isneginf(lse[0, :, 0]))
+        assert torch.all(o[0, :, 1, 5] == float("inf"))
+
+
 def test_not_finite_values_in_a_chain():
     c = problem(1, 2, 2, 140, 128, 32, [60], BF, seed=7)
     clean = {n: None if t is None else t.clone() for n, t in c.items()}
