@@ -651,7 +651,7 @@ fa_paged_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                     const unsigned bads = __ballot_sync(0xffffffffu, bad && half == 0);
                     if (lane == 0) {
                         bars->bad[gj & 15] = bads;
-                        if (bads) atomicExch(&g_status, 6);
+                        if (bads) report_bad_page();
                     }
                 }
                 const int y = key & (page - 1);

@@ -149,6 +149,10 @@ struct PageTable {
     const int *new_len;    // [B] new tokens (nullptr: T)
 };
 
+// FA_ERR_BAD_PAGE in the status word, unless it already holds something (a wait that gave up is
+// the graver: it takes the word whatever it holds).
+__device__ __forceinline__ void report_bad_page() { atomicCAS(&g_status, 0, 6); }
+
 // Tokens held before the call and new tokens of sequence b, made safe: 0 <= past,
 // past + fresh <= the table's capacity, fresh <= T.
 __device__ __forceinline__ void page_lengths(const PageTable &t, int T, int b, int &past,
@@ -165,7 +169,7 @@ __device__ __forceinline__ void page_lengths(const PageTable &t, int T, int b, i
 __device__ __forceinline__ void page_lengths_check(const PageTable &t, int T, int b) {
     const int pl = __ldg(t.cache_len + b), nl = t.new_len ? __ldg(t.new_len + b) : T;
     if (pl < 0 || nl < 0 || nl > T || pl + (long long)nl > ((long long)t.max_blocks << t.page_shift))
-        atomicExch(&g_status, 6);
+        report_bad_page();
 }
 
 struct AppendParams {
@@ -208,7 +212,7 @@ __global__ void __launch_bounds__(256) fa_kv_append_kernel(const AppendParams p)
         if (block < p.pt.max_blocks) page = __ldg(p.pt.table + (long long)b * p.pt.max_blocks + block);
         if (page < 0 || page >= p.pt.num_pages) {
             page = -1;
-            atomicExch(&g_status, 6);
+            report_bad_page();
         }
     }
     const bool turn = p.turns != nullptr && c * 16 < p.rot && h0 < p.H + p.Hk;

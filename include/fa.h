@@ -125,9 +125,8 @@ FA_API const char *fa_last_cuda_error(void);
 /*
  * Synchronises `stream`, then reads and clears the current device's status word.
  * Returns FA_OK, FA_ERR_TIMEOUT if some kernel gave up a bounded wait since the
- * last call, FA_ERR_BAD_PAGE if a paged-cache call met a page number or a length outside
- * the cache (the later of the two where both happened), or FA_ERR_CUDA if the
- * synchronisation failed.
+ * last call, FA_ERR_BAD_PAGE if no wait did but a paged-cache call met a page number or a
+ * length outside the cache, or FA_ERR_CUDA if the synchronisation failed.
  */
 FA_API int fa_get_device_status(void *stream);
 
