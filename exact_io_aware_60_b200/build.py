@@ -16,6 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfa.so")
 BINDING = os.path.join(PKG, "_fa_binding.so")
+BINDING_STAMP = os.path.join(PKG, "_fa_binding.stamp")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -43,27 +45,48 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def build_binding(force: bool = False, verbose: bool = False) -> str:
-    src = os.path.join(CSRC, "binding.cpp")
-    if not force and os.path.exists(BINDING) and os.path.getmtime(src) <= os.path.getmtime(BINDING):
-        return BINDING
+def binding_command(out: str):
+    """(command, stamp): the stamp names all that the binding is compiled against, the sources
+    aside; it reads tensors through torch's own classes, whose layout is a version's."""
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension as ext
-    tmp = BINDING + f".tmp{os.getpid()}"
-    libs = ext.library_paths(device_type="cuda")
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f'-DFA_TORCH_VERSION="{torch.__version__}"', f"-I{INCLUDE}",
            *(f"-I{p}" for p in ext.include_paths(device_type="cuda")),
-           f"-I{sysconfig.get_paths()['include']}", src, "-o", tmp, *(f"-L{p}" for p in libs),
+           f"-I{sysconfig.get_paths()['include']}", BINDING_SRC, "-o", out,
+           *(f"-L{p}" for p in ext.library_paths(device_type="cuda")),
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    flags = [x for x in cmd if x.startswith(("-O", "-D", "-s", "-f", "-l"))]
+    return cmd, " ".join([torch.__version__, sysconfig.get_config_var("SOABI") or "", *flags]) + "\n"
+
+
+def binding_up_to_date(stamp: str) -> bool:
+    try:
+        with open(BINDING_STAMP) as f:
+            if f.read() != stamp:
+                return False
+        t = os.path.getmtime(BINDING)
+    except OSError:
+        return False
+    return all(os.path.getmtime(s) <= t for s in (BINDING_SRC, os.path.join(INCLUDE, "fa.h")))
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd, stamp = binding_command(tmp)
+    if not force and binding_up_to_date(stamp):
+        return BINDING
     res = subprocess.run(cmd, capture_output=True, text=True)
     if verbose or res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
     if res.returncode != 0:
         raise RuntimeError("g++ failed building _fa_binding.so")
     os.replace(tmp, BINDING)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(stamp)
     return BINDING
 
 

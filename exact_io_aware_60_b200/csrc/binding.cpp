@@ -14,20 +14,14 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include "fa.h"
+
 namespace {
 
-using RopeFn = int (*)(const void *, void *, const void *, void *, int, int, int, int, int,
-                       const long long *, const long long *, const long long *, const long long *,
-                       const int *, int, const unsigned long long *, int, int, float, int, void *);
-using AppendFn = int (*)(const void *, const void *, void *, void *, const void *, void *, int, int,
-                         int, int, int, const long long *, const long long *, const long long *,
-                         const long long *, const long long *, const long long *, int, int,
-                         const int *, int, const int *, const int *, const int *,
-                         const unsigned long long *, int, int, float, int, void *);
-using PagedFn = int (*)(const void *, const void *, const void *, void *, float *, int, int, int, int,
-                        int, const long long *, const long long *, const long long *,
-                        const long long *, int, int, const int *, int, const int *, const int *,
-                        const unsigned char *, int, float, int, void *, size_t, void *);
+// (called by address: the library is loaded by the caller)
+using RopeFn = decltype(&fa_rope);
+using AppendFn = decltype(&fa_kv_append);
+using PagedFn = decltype(&fa_fwd_paged);
 
 // A [n0, n1, n2, d] tensor with d contiguous.
 struct Rows {
@@ -297,4 +291,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fa_binding", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fa_binding() { return PyModule_Create(&module); }
+// built_for: the torch version whose headers this was compiled against.
+PyMODINIT_FUNC PyInit__fa_binding() {
+    PyObject *m = PyModule_Create(&module);
+    if (m != nullptr && PyModule_AddStringConstant(m, "built_for", FA_TORCH_VERSION) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -16,17 +16,35 @@ import dataclasses
 import math
 import os
 import threading
+import warnings
 from typing import Optional
 
 import torch
 
-try:
-    from . import _fa_binding as _quick  # (needs torch's libraries, loaded above)
-except ImportError:                      # not built: the same calls by ctypes
-    _quick = None
-
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfa.so")
+
+
+def _load_quick():
+    """The compiled binding of the serving calls, or None (the same calls go by ctypes): it is not
+    built, or, which is said, it was built for another torch or Python."""
+    why = None
+    try:
+        from . import _fa_binding as quick  # (needs torch's libraries, loaded above)
+        if getattr(quick, "built_for", None) == torch.__version__:
+            return quick
+        why = f"built for torch {getattr(quick, 'built_for', '?')}, this is {torch.__version__}"
+    except ImportError as e:
+        if os.path.exists(os.path.join(_HERE, "_fa_binding.so")):
+            why = str(e)
+    if why:
+        warnings.warn(f"_fa_binding.so is not used ({why}); the serving calls go by ctypes, some "
+                      "5 us of host time each slower.  Build it again: python -m "
+                      f"{__package__}.build", RuntimeWarning, stacklevel=2)
+    return None
+
+
+_quick = _load_quick()
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = range(5)
 FA_ERR_SCRATCH_LIMIT = 5
