@@ -463,7 +463,12 @@ def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: str = "non
     if scaling == "ntk":
         if rot_dim == 2:
             raise FAError(FA_ERR_INVALID_ARG, "rope_frequencies: ntk needs rot_dim > 2")
-        base = base * factor ** (rot_dim / (rot_dim - 2))
+        try:
+            base = base * factor ** (rot_dim / (rot_dim - 2))
+        except OverflowError:
+            base = math.inf
+        if math.isinf(base):
+            raise FAError(FA_ERR_INVALID_ARG, "rope_frequencies: ntk's base overflows")
     f = [base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
     if scaling == "linear":
         return [x / factor for x in f], 1.0
@@ -506,7 +511,8 @@ def rope_plan(rot_dim: int, *, layout: str = "half", base: float = 10000.0, scal
         raise FAError(FA_ERR_INVALID_ARG, "rope_plan: magnitude must be finite and > 0")
     turns = []
     for x in freq:
-        u = int(round(x / (2.0 * math.pi) * 2.0 ** 64)) % (1 << 64)
+        # (whole turns drop out first, exactly: any finite angle has its 64 bits)
+        u = int(round(math.fmod(x / (2.0 * math.pi), 1.0) * 2.0 ** 64)) % (1 << 64)
         turns.append(u - (1 << 64) if u >= 1 << 63 else u)
     if device is None:
         device = torch.device("cuda", torch.cuda.current_device())

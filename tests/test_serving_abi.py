@@ -1,6 +1,7 @@
 """Refusals of the rotary and paged-cache entry points, on the host alone: C status codes with
 addresses that are never dereferenced, the binding's own checks, and the frequency plans."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -166,3 +167,18 @@ def test_quick_binding_leaves_other_calls_alone():
     assert fa._quick.append(0, x, x, x, x, i[None], i, None, None, None, None, None, 0, False, 1.0,
                             None) is None
     assert fa._quick.paged(0, x, x, x, i[None], i, None, x, x, None, x, "scale", None) is None
+
+
+@pytest.mark.parametrize("x", [1e308, -1e308, 1e290, 3e18, -0.75, 5e-324, 0.0])
+def test_plan_takes_any_finite_angle(x):
+    bits = fa.rope_plan(16, frequencies=[x] * 8, device="cpu").turns.tolist()
+    turn = Fraction(x / (2.0 * math.pi))
+    want = (turn * 2 ** 64) % 2 ** 64
+    off = (bits[0] - want + 2 ** 63) % 2 ** 64 - 2 ** 63
+    assert bits == bits[:1] * 8 and abs(off) <= Fraction(1, 2)
+
+
+@pytest.mark.parametrize("kw", [dict(factor=1e300), dict(factor=1e200, base=1e100)])
+def test_an_ntk_base_that_overflows_is_refused(kw):
+    with pytest.raises(fa.FAError):
+        fa.rope_plan(16, scaling="ntk", device="cpu", **kw)
