@@ -1319,6 +1319,10 @@ int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *
     const int G = H / Hk;
     const PagedShape sh = paged_shape(G, T);
     const long long cap_tiles = ((long long)max_blocks * page_size + 127) / 128;
+    // Every CTA sums up the sequences' work, 32 of them in about 0.5 us, and the last goes through
+    // them again to its share, while its other warps wait: 0.6 s for the largest batch, within the
+    // 2 s of a wait.  (2^18 sequences without a new token: 14.0 ms, 2.5 where nothing is summed up.)
+    if (B > (1 << 24)) return FA_ERR_UNSUPPORTED;
     // units of work are counted in 32 bits
     if ((double)sh.row_tiles * Hk * B * (cap_tiles + fa::kItemCost) >= (double)(1LL << 31))
         return FA_ERR_UNSUPPORTED;

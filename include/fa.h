@@ -408,8 +408,8 @@ FA_API int fa_kv_append(const void *k, const void *v, void *k_cache, void *v_cac
  * table; page numbers outside [0, num_pages) make their keys invisible; both report
  * FA_ERR_BAD_PAGE in the device status word.
  * H must be a multiple of Hk.  Returns FA_ERR_INVALID_ARG for bad arguments or a missing,
- * small or misaligned workspace, FA_ERR_UNSUPPORTED for sizes beyond fa_rope's or when the
- * table's room comes to 2^31 or more tiles of 128 keys over all sequences, key/value heads
+ * small or misaligned workspace, FA_ERR_UNSUPPORTED for sizes beyond fa_rope's, more than
+ * 2^24 sequences or when the table's room comes to 2^31 or more tiles of 128 keys over all sequences, key/value heads
  * and row tiles (of up to 256 rows, T * H / Hk in all).  Forward only.
  */
 FA_API size_t fa_fwd_paged_workspace_bytes(int B, int H, int Hk, int T, int d);

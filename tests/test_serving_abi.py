@@ -182,3 +182,7 @@ def test_plan_takes_any_finite_angle(x):
 def test_an_ntk_base_that_overflows_is_refused(kw):
     with pytest.raises(fa.FAError):
         fa.rope_plan(16, scaling="ntk", device="cpu", **kw)
+
+
+def test_paged_refuses_batches_that_outlast_a_wait():
+    assert paged(B=(1 << 24) + 1, H=1, Hk=1, T=1, blocks=100) == NO
