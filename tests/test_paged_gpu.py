@@ -136,6 +136,51 @@ def test_long_shares(case):
     assert torch.isfinite(o.float()).all()
 
 
+def against_heads(c, heads):
+    """against_reference for some of the heads (long problems)."""
+    o, lse = run(c)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK
+    wo, wl, ob, lb = R.paged(c["q"], c["kc"], c["vc"], c["table"], c["cache_len"], c["new_len"],
+                             c["tree"], c["q"].shape[-1] ** -0.5, heads)
+    R.check("o", o[:, heads], wo[:, heads], (ob + R.rounding(wo, c["q"].dtype))[:, heads])
+    R.check("lse", lse[:, heads], wl[:, heads], lb[:, heads])
+    assert torch.isfinite(o.float()).all()
+
+
+@pytest.mark.parametrize("case", [
+    (1, 2, 4, 2500, 128, 64, [0], BF, None),
+    (2, 2, 2, 2100, 64, 16, [300, 0], FP, [2100, 1777]),
+    (1, 4, 1, 3333, 128, 128, [500], FP, None),
+    (3, 1, 5, 1031, 64, 32, [0, 127, 1], BF, [1031, 900, 1]),
+], ids=lambda c: "-".join(str(x) for x in c[:6]))
+def test_prompts_over_an_empty_or_short_cache(case):
+    B, Hk, G, T, d, page, lens, dtype, new = case
+    c = problem(B, Hk, G, T, d, page, lens, dtype, new=new, seed=T)
+    against_heads(c, [0, Hk * G - 1])
+
+
+@pytest.mark.parametrize("tree", [False, True], ids=["chain", "tree"])
+@pytest.mark.parametrize("wide", [False, True], ids=["tight", "wide"])
+@pytest.mark.parametrize("T,G,d,news", [
+    # new tokens on both sides of a copy's, a warp's, a row tile's and an item's end
+    (8, 4, 64, [8, 7, 1, 2]), (8, 4, 128, [7, 8, 3, 1]), (16, 4, 128, [8, 9, 16, 1]), (15, 4, 64, [8, 7, 15, 2]),
+    (25, 5, 64, [6, 7, 12, 13, 25]), (25, 5, 128, [6, 7, 13, 19, 25]),
+    (61, 3, 64, [42, 43, 61, 41]), (61, 3, 128, [42, 43, 61, 11]),
+    (100, 3, 64, [84, 85, 42, 100, 43]), (100, 3, 128, [85, 84, 43, 100, 42]),
+])
+def test_new_tokens_end_about_a_row_tile(T, G, d, news, wide, tree):
+    """Ragged new tokens in cut items of every form."""
+    B, dtype = len(news), FP if d == 64 else BF
+    c = problem(B, 2, G, T, d, 32, [3000 + 517 * i for i in range(B)], dtype, new=news, tree=tree, seed=T + d)
+    if wide:
+        c = widen(c, 800)
+    against_heads(c, [0, G, 2 * G - 1])
+    o, lse = run(c)
+    for b, n in enumerate(news):
+        assert torch.all(o[b, :, n:] == 0) and torch.all(torch.isneginf(lse[b, :, n:]))
+
+
 def widen(c, tiles):
     """The same problem in a table with room for `tiles` tiles of 128 keys; the entries behind the
     sequences' are no pages at all.  (The room decides between one and two softmax groups, and
