@@ -1348,17 +1348,18 @@ int fa_fwd_paged(const void *q, const void *k_cache, const void *v_cache, void *
     p.TPT = sh.TPT;
     // Short items are not cut: with up to 64 rows a tile more takes 0.5 us (d = 64; 0.6 at 128),
     // without copies of the rows 1.1 to 2 us, against 4 to 5 us for the merge and the pieces.
-    // Measured, cut and not (one token, 4 rows, d = 64): 2 items of 5 tiles 8.5 and 7.9 us, of 8
-    // tiles 8.6 and 9.8; 32 items of 8 tiles 11.2 and 10.2; 256 items of 10 tiles 28.1 and 23.1;
-    // 80 rows, 16 items of 4 tiles 12.9 and 12.6 (d = 128), of 5 tiles 11.6 and 12.8 (d = 64).
+    // Measured, cut and not (one token, 4 rows, d = 64): 2 items of 5 tiles 8.5 and 8.0 us, of 8
+    // tiles 8.8 and 9.9; 32 items of 8 tiles 10.9 and 10.3; 256 items of 10 tiles 27.5 and 23.6;
+    // 80 rows, 16 items of 4 tiles 12.5 and 12.2 (d = 128), of 5 tiles 11.5 and 11.7 (d = 64).
+    // (The lengths are not known here: items that are as short in a table with more room are cut.)
     const long long items = sh.row_tiles * Hk * B;
     p.uncut = cap_tiles <= (sh.rows > 64 ? 4 : items < 32 ? 6 : 10);
     // Two groups of softmax warps (d = 64, one row tile of 65 to 128 rows) take less time a tile
     // and more an item or piece of one: worth it from about 4 tiles a piece on, of which there
-    // are items + ctas.  One and two groups, 128 rows, us: 512 items of 2 tiles 26.1 and 27.3, of
-    // 5 tiles 48.5 and 48.8, of 8 tiles 62.6 and 58.3; 128 items of 5 tiles 18.9 and 19.5, of 10
-    // tiles 27.3 and 26.3, of 32 tiles 54.7 and 46.3; 8 items of 63 tiles 18.7 and 18.8, of 126
-    // tiles 23.9 and 22.7.  (The lengths are not known here: where a table has far more room
+    // are items + ctas.  One and two groups, 128 rows, us: 512 items of 2 tiles 25.3 and 26.5, of
+    // 5 tiles 46.8 and 46.8, of 8 tiles 60.0 and 56.2; 128 items of 5 tiles 18.2 and 18.8, of 10
+    // tiles 26.1 and 25.7, of 32 tiles 51.7 and 44.4; 8 items of 63 tiles 17.7 and 17.7, of 126
+    // tiles 22.5 and 21.5.  (The lengths are not known here: where a table has far more room
     // than its sequences take, the choice costs up to 9%.)
     const bool two_groups = d == 64 && sh.rows == 128 && items * cap_tiles >= 4 * (items + ctas);
     p.row_tiles = (int)sh.row_tiles;

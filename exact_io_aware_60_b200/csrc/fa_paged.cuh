@@ -11,10 +11,17 @@
 // Bound by memory for up to about 256 rows per key/value head (4 R flop per 2 bytes against
 // 260 flop per byte of the card): a 128-key tile of one SM's share of HBM takes 1.5 us at
 // d = 128, 0.75 us at d = 64.  Measured on B200 (kernels in a graph, three sets of inputs in
-// turn): one token for each of 8 sequences of 32768 keys, 16 heads over 4, d = 128, 88 us, 6.1
-// TB/s = 0.93 of the measured copy rate; at d = 64 51 us, 0.80; a chunk of 512 tokens against
-// 15872 keys, 16 heads, d = 128, 85 us, 795 TFLOP/s; 16 sequences of up to 8000 keys, trees of
+// turn): one token for each of 8 sequences of 32768 keys, 16 heads over 4, d = 128, 86 us, 6.3
+// TB/s = 0.96 of the measured copy rate; at d = 64 50 us, 0.82; a chunk of 512 tokens against
+// 15872 keys, 16 heads, d = 128, 83 us, 810 TFLOP/s; 16 sequences of up to 8000 keys, trees of
 // 16 tokens, 32 heads over 8, pages of 16, 58 us.
+//
+// Precision: scores, maxima, sums, O and the pieces are fp32.  The weights are rounded to the
+// element type, as the tensor cores take one 16-bit type for P and V and a second product for
+// the rest of P would double the time of P V; O is divided by the sum of the rounded weights,
+// so that their rounding has no bias.  Against 64 bits O is then off by 1.3 to 1.4 times what
+// fp32 weights give with the same last rounding (bf16 2.2e-3 against 1.7e-3 of the norm, fp16
+// 2.8e-4 against 2.1e-4); the log-sum-exp is of the unrounded weights.
 //
 // Work: the 128-key tiles of all (sequence, key/value head, row tile) items form one flat
 // list that is cut into equal shares, one per CTA, wherever the cuts fall (lengths are only
@@ -36,7 +43,7 @@
 // At d = 64, where a tile's bytes take less than its 128 exponentials a row, one row tile can
 // have two groups of softmax warps (KS = 2) that take the key tiles in turn, each with an O of
 // its own, merged in the epilogue (16 sequences of 4000 keys, 32 new tokens, 32 heads over 8:
-// 55 us with one group, 46 with two; of 600 keys 18.9 and 19.5, so that fa_fwd_paged chooses).
+// 52 us with one group, 44 with two; of 600 keys 18.2 and 18.8, so that fa_fwd_paged chooses).
 // Many rows (RT = 2): two tiles of 128 rows share every K and V tile, each with softmax warps
 // of its own, so that one tile's products run beside the other's exponentials.
 #pragma once

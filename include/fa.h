@@ -366,9 +366,9 @@ FA_API int fa_rope_bwd(const void *dq_rot, void *dq, const void *dk_rot, void *d
  *                 other three are then ignored).
  * A negative length counts as 0, a new_len above T as T.  A token whose slot is behind
  * max_blocks * page_size, or whose page number is outside [0, num_pages), is not written.
- * All of these report FA_ERR_BAD_PAGE in the device status word.  Two tokens of one call must not share a slot (a page listed by
- * two sequences may be shared only where neither writes).  Sizes as fa_rope, with
- * H + 2 Hk heads; max_blocks * page_size < 2^31 - 256.
+ * All of these report FA_ERR_BAD_PAGE in the device status word.  Two tokens of one call must
+ * not share a slot (a page listed by two sequences may be shared only where neither writes).
+ * Sizes as fa_rope, with H + 2 Hk heads; max_blocks * page_size < 2^31 - 256.
  */
 FA_API int fa_kv_append(const void *k, const void *v, void *k_cache, void *v_cache, const void *q,
                         void *q_out, int B, int H, int Hk, int T, int d,
@@ -399,6 +399,9 @@ FA_API int fa_kv_append(const void *k, const void *v, void *k_cache, void *v_cac
  *                 256-byte aligned, contents irrelevant and clobbered; it must not be shared
  *                 by calls that may run at the same time.  The size depends on the current
  *                 device: call both on the same one.
+ * Scores, sums and the output's accumulation are fp32; the weights are rounded to the element
+ * type for the product with V and divided by the sum of the rounded ones, the output is
+ * rounded once more.
  * Rows that see no key, rows t >= new_len[b] among them, get O = 0, LSE = -inf.  Slots from
  * cache_len[b] + new_len[b] on are never used, whatever they hold; keys that a row's mask
  * hides do not touch that row either, infinities and NaN in them included.  An infinite value
